@@ -2,13 +2,15 @@
 
     python -m gated_delta_rule_89_b200.build
 
-compiles every ``csrc/*.cu`` into one shared library next to this file.  The
+compiles every ``csrc/*.cu`` (in parallel, into objects under ``_build/``; only
+what changed) and links them into one shared library next to this file.  The
 CUDA runtime is linked statically, so the library runs beside any PyTorch
 build; the driver API (tensor maps) is reached through the runtime's entry
 point query, so no link against libcuda is needed.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import shutil
@@ -18,6 +20,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdr.so")
+OBJ = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -47,13 +50,29 @@ def needs_build() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
-    cmd = [nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
-           "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
-           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
-           *extra, "-o", LIB + ".tmp", *sources()]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+    os.makedirs(OBJ, exist_ok=True)
+    headers = [p for p in deps() if not p.endswith(".cu")] + [os.path.abspath(__file__)]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    def compile_one(src):
+        obj = os.path.join(OBJ, os.path.basename(src) + ".o")
+        if not force and not extra and os.path.exists(obj) and \
+                all(os.path.getmtime(obj) >= os.path.getmtime(p) for p in [src, *headers]):
+            return obj
+        run([nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
+             "-Xcompiler", "-fPIC,-fvisibility=hidden",
+             "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
+             *extra, "-c", "-o", obj + ".tmp", src])
+        os.replace(obj + ".tmp", obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        objects = list(pool.map(compile_one, sources()))
+    run([nvcc(), *ARCH, "-Xcompiler", "-fPIC", "-shared", "-o", LIB + ".tmp", *objects])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 
