@@ -21,7 +21,8 @@ import torch
 
 __all__ = ["chunk_fwd", "recurrent_step", "chunk_fwd_workspace_size", "chunk_fwd_prologue", "chunk_fwd_gdr2",
            "chunk_fwd_gated", "chunk_bwd",
-           "recurrent_step_gdr2", "GDRError", "library_path",
+           "recurrent_step_gdr2", "short_conv_fwd", "short_conv_step", "short_conv_bwd", "ssm_scan_fwd",
+           "ssm_scan_step", "ssm_scan_fwd_workspace_size", "GDRError", "library_path",
            "last_launch_count", "device_status", "GATE_PER_CHANNEL", "GATE_SCALAR"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +73,16 @@ def lib() -> ctypes.CDLL:
         L.gdr2_chunk_fwd_workspace_size.restype = Z
         L.gdr2_recurrent_step.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P]
         L.gdr2_recurrent_step.restype = I
+        S = ctypes.c_longlong
+        L.gdr_short_conv_fwd.argtypes = [P] * 8 + [I] * 7 + [P]
+        L.gdr_short_conv_step.argtypes = [P] * 5 + [S] + [I] * 5 + [P]
+        L.gdr_short_conv_bwd.argtypes = [P] * 14 + [I] * 7 + [P, Z, P]
+        L.gdr_short_conv_bwd_workspace_size.argtypes = [I] * 6
+        L.gdr_short_conv_bwd_workspace_size.restype = Z
+        L.gdr_ssm_scan_fwd.argtypes = [P] * 13 + [I] * 7 + [P, Z, P]
+        L.gdr_ssm_scan_fwd_workspace_size.argtypes = [I] * 6
+        L.gdr_ssm_scan_fwd_workspace_size.restype = Z
+        L.gdr_ssm_scan_step.argtypes = [P] * 11 + [I] * 6 + [P]
         L.gdr_status_string.argtypes = [I]
         L.gdr_status_string.restype = ctypes.c_char_p
         L.gdr_last_cuda_error.restype = I
@@ -513,3 +524,7 @@ def chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
 def chunk_bwd_workspace_size(B, H, T, dk, dv, C=64, gate="per_channel", dtype=torch.bfloat16) -> int:
     g = GATE_PER_CHANNEL if gate == "per_channel" else GATE_SCALAR
     return int(lib().gdr_chunk_bwd_workspace_size(B, H, T, dk, dv, C, g, _DTYPES[dtype]))
+
+
+from .ssm import (short_conv_bwd, short_conv_fwd, short_conv_step, ssm_scan_fwd,   # noqa: E402
+                  ssm_scan_fwd_workspace_size, ssm_scan_step)

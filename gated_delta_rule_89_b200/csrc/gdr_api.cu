@@ -4,6 +4,7 @@
 
 #include "gdr.h"
 #include "gdr_internal.cuh"
+#include "ssm_internal.cuh"
 
 #define GDR_API extern "C" __attribute__((visibility("default")))
 
@@ -419,5 +420,210 @@ GDR_API int gdr_recurrent_step(const void *q, const void *k, const void *v, cons
     if (const int gs = gate_guard(g, gate_elems((long long)B * H, 1, dk, gate_mode), st)) return gs;
     int launches = 0;
     cudaError_t e = gdr::launch_recurrent_step(a, st, &launches);
+    return finish(e, launches);
+}
+
+// ---------------------------------------------- short convolution and state space scan
+
+namespace {
+
+// Bytes of one element, 0 for a bad dtype.
+size_t elem_bytes(int dtype) { return dtype == GDR_F32 ? 4 : dtype == GDR_BF16 ? 2 : 0; }
+
+bool any_misaligned(const void *const *p, int n, size_t bytes)
+{
+    for (int i = 0; i < n; ++i)
+        if (p[i] && !gdr::aligned_to(p[i], bytes)) return true;
+    return false;
+}
+
+bool any_null(const void *const *p, int n)
+{
+    for (int i = 0; i < n; ++i)
+        if (!p[i]) return true;
+    return false;
+}
+
+bool any_negative(const long long *s, int n)
+{
+    for (int i = 0; s && i < n; ++i)
+        if (s[i] < 0) return true;
+    return false;
+}
+
+// Sizes both operators share; the limits keep every token index, block count
+// and channel index inside 32 bits (offsets are 64-bit throughout).
+int sequence_sizes(int B, int T, long long D)
+{
+    if (B < 0 || T < 0 || D < 0) return GDR_ERR_INVALID_ARG;
+    if (B > (1 << 20) || T >= (1 << 30) || D > (1 << 20)) return GDR_ERR_UNSUPPORTED;
+    if ((long long)B * (T ? T : 1) * (D ? D : 1) >= (1LL << 40)) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+int conv_sizes(int B, int H, int T, int d, int W, int act, int dtype)
+{
+    if (H < 0 || d < 0 || W <= 0 || !elem_bytes(dtype)) return GDR_ERR_INVALID_ARG;
+    if (act != GDR_ACT_NONE && act != GDR_ACT_SILU) return GDR_ERR_INVALID_ARG;
+    if (W < 2 || W > 4) return GDR_ERR_UNSUPPORTED;
+    return sequence_sizes(B, T, (long long)H * d);
+}
+
+gdr::RowStrides rows_or_dense(const long long *s, int H, int T, int d)
+{
+    if (s) return {s[0], s[1], s[2]};
+    return {(long long)H * T * d, (long long)T * d, d};
+}
+
+int scan_sizes(int B, int T, int D, int G, int N, int dtype)
+{
+    if (!elem_bytes(dtype) || G <= 0 || N <= 0) return GDR_ERR_INVALID_ARG;
+    if (const int e = sequence_sizes(B, T, D)) return e;
+    if (D % G) return GDR_ERR_INVALID_ARG;
+    if (N != 8 && N != 16 && N != 32 && N != 64) return GDR_ERR_UNSUPPORTED;
+    if ((long long)B * G * ((D / G + 7) / 8) >= (1LL << 31)) return GDR_ERR_UNSUPPORTED;
+    if ((long long)B * D * N >= (1LL << 40)) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+gdr::BatchToken tokens_or_dense(const long long *s, int T, long long row)
+{
+    if (s) return {s[0], s[1]};
+    return {(long long)T * row, row};
+}
+
+int nothing_to_do()
+{
+    tl_last_launches = 0;
+    return GDR_OK;
+}
+
+}  // namespace
+
+GDR_API int gdr_short_conv_fwd(const void *x, const float *weight, const float *bias, const void *state,
+                               const int *lengths, void *y, void *state_out, const long long *x_strides,
+                               int B, int H, int T, int d, int W, int act, int dtype, void *stream)
+{
+    if (const int e = conv_sizes(B, H, T, d, W, act, dtype)) return e;
+    if (any_negative(x_strides, 3)) return GDR_ERR_INVALID_ARG;
+    if (B == 0 || H == 0 || d == 0 || (T == 0 && !state_out)) return nothing_to_do();
+    if (!weight || (T > 0 && (!x || !y))) return GDR_ERR_INVALID_ARG;
+    const void *rows[] = {x, state, y, state_out}, *words[] = {weight, bias, lengths};
+    if (any_misaligned(rows, 4, elem_bytes(dtype)) || any_misaligned(words, 3, 4)) return GDR_ERR_ALIGNMENT;
+    gdr::ConvArgs a = {x, rows_or_dense(x_strides, H, T, d), weight, bias, state, lengths, y, state_out,
+                       B, H, T, d, W, act == GDR_ACT_SILU, dtype == GDR_BF16};
+    int launches = 0;
+    const cudaError_t e = gdr::launch_short_conv_fwd(a, static_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+GDR_API int gdr_short_conv_step(const void *x, const float *weight, const float *bias, void *state, void *y,
+                                long long x_stride, int B, int D, int W, int act, int dtype, void *stream)
+{
+    if (const int e = conv_sizes(B, 1, 1, D, W, act, dtype)) return e;
+    if (x_stride < 0) return GDR_ERR_INVALID_ARG;
+    if (B == 0 || D == 0) return nothing_to_do();
+    if (!x || !weight || !state || !y) return GDR_ERR_INVALID_ARG;
+    const void *rows[] = {x, state, y}, *words[] = {weight, bias};
+    if (any_misaligned(rows, 3, elem_bytes(dtype)) || any_misaligned(words, 2, 4)) return GDR_ERR_ALIGNMENT;
+    gdr::ConvArgs a = {x, {x_stride, 0, 0}, weight, bias, state, nullptr, y, state,
+                       B, 1, 1, D, W, act == GDR_ACT_SILU, dtype == GDR_BF16};
+    int launches = 0;
+    const cudaError_t e = gdr::launch_short_conv_step(a, static_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+GDR_API size_t gdr_short_conv_bwd_workspace_size(int B, int H, int T, int d, int W, int dtype)
+{
+    if (conv_sizes(B, H, T, d, W, GDR_ACT_NONE, dtype) || B == 0 || H == 0 || d == 0) return 0;
+    return gdr::short_conv_bwd_workspace_bytes(B, H, T, d, W);
+}
+
+GDR_API int gdr_short_conv_bwd(const void *x, const float *weight, const float *bias, const void *state,
+                               const int *lengths, const void *dy, const void *dstate_out,
+                               void *dx, float *dweight, float *dbias, void *dstate,
+                               const long long *x_strides, const long long *dy_strides, const long long *dx_strides,
+                               int B, int H, int T, int d, int W, int act, int dtype,
+                               void *workspace, size_t ws_bytes, void *stream)
+{
+    if (const int e = conv_sizes(B, H, T, d, W, act, dtype)) return e;
+    if (any_negative(x_strides, 3) || any_negative(dy_strides, 3) || any_negative(dx_strides, 3))
+        return GDR_ERR_INVALID_ARG;
+    if (H == 0 || d == 0) return nothing_to_do();
+    if (!weight || !dweight || (B > 0 && T > 0 && (!x || !dy || !dx))) return GDR_ERR_INVALID_ARG;
+    const void *rows[] = {x, dy, dx, state, dstate_out, dstate};
+    const void *words[] = {weight, bias, lengths, dweight, dbias};
+    if (any_misaligned(rows, 6, elem_bytes(dtype)) || any_misaligned(words, 5, 4) || !aligned16(workspace))
+        return GDR_ERR_ALIGNMENT;
+    const size_t need = gdr_short_conv_bwd_workspace_size(B, H, T, d, W, dtype);
+    if (ws_bytes < need || (need && !workspace)) return GDR_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (B == 0) {   // the sums over no rows
+        cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)H * d * W, st);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)H * d, st);
+        return finish(e, 0);
+    }
+    gdr::ConvBwdArgs a = {x, dy, rows_or_dense(x_strides, H, T, d), rows_or_dense(dy_strides, H, T, d),
+                          rows_or_dense(dx_strides, H, T, d), weight, bias, state, dstate_out, lengths, dx, dstate,
+                          dweight, dbias, B, H, T, d, W, act == GDR_ACT_SILU, dtype == GDR_BF16, workspace};
+    int launches = 0;
+    const cudaError_t e = gdr::launch_short_conv_bwd(a, st, &launches);
+    return finish(e, launches);
+}
+
+GDR_API size_t gdr_ssm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dtype)
+{
+    if (scan_sizes(B, T, D, G, N, dtype) || B == 0 || T == 0 || D == 0) return 0;
+    return gdr::ssm_scan_fwd_workspace_bytes(B, T, D, G, N);
+}
+
+GDR_API int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                             const float *D_skip, const void *z, const float *dt_bias, const float *h0,
+                             const int *lengths, void *y, float *h_T, const long long *strides,
+                             int B, int T, int D, int G, int N, int dt_softplus, int dtype,
+                             void *workspace, size_t ws_bytes, void *stream)
+{
+    if (const int e = scan_sizes(B, T, D, G, N, dtype)) return e;
+    if (any_negative(strides, 10)) return GDR_ERR_INVALID_ARG;
+    if (B == 0 || D == 0 || (T == 0 && !h_T)) return nothing_to_do();
+    const void *need[] = {x, dt, Bm, Cm, y};
+    if (!A || (T > 0 && any_null(need, 5))) return GDR_ERR_INVALID_ARG;
+    const void *rows[] = {x, dt, Bm, Cm, z, y}, *words[] = {D_skip, dt_bias, lengths};
+    const void *lines[] = {A, h0, h_T, workspace};
+    if (any_misaligned(rows, 6, elem_bytes(dtype)) || any_misaligned(words, 3, 4) || any_misaligned(lines, 4, 16))
+        return GDR_ERR_ALIGNMENT;
+    const size_t ws_need = gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N, dtype);
+    if (ws_bytes < ws_need || (ws_need && !workspace)) return GDR_ERR_INVALID_ARG;
+    const long long *s = strides;
+    gdr::ScanArgs a = {x, dt, Bm, Cm, z, tokens_or_dense(s, T, D), tokens_or_dense(s ? s + 2 : s, T, D),
+                       tokens_or_dense(s ? s + 4 : s, T, (long long)G * N),
+                       tokens_or_dense(s ? s + 6 : s, T, (long long)G * N), tokens_or_dense(s ? s + 8 : s, T, D),
+                       A, D_skip, dt_bias, h0, lengths, y, h_T, B, T, D, G, N, dt_softplus != 0, dtype == GDR_BF16,
+                       workspace};
+    int launches = 0;
+    const cudaError_t e = gdr::launch_ssm_scan_fwd(a, static_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+GDR_API int gdr_ssm_scan_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                              const float *D_skip, const void *z, const float *dt_bias, float *h, void *y,
+                              const long long *strides, int B, int D, int G, int N, int dt_softplus, int dtype,
+                              void *stream)
+{
+    if (const int e = scan_sizes(B, 1, D, G, N, dtype)) return e;
+    if (any_negative(strides, 5)) return GDR_ERR_INVALID_ARG;
+    if (B == 0 || D == 0) return nothing_to_do();
+    const void *need[] = {x, dt, A, Bm, Cm, h, y};
+    if (any_null(need, 7)) return GDR_ERR_INVALID_ARG;
+    const void *rows[] = {x, dt, Bm, Cm, z, y}, *words[] = {D_skip, dt_bias}, *lines[] = {A, h};
+    if (any_misaligned(rows, 6, elem_bytes(dtype)) || any_misaligned(words, 2, 4) || any_misaligned(lines, 2, 16))
+        return GDR_ERR_ALIGNMENT;
+    const long long dense[] = {D, D, (long long)G * N, (long long)G * N, D};
+    const long long *s = strides ? strides : dense;
+    gdr::ScanArgs a = {x, dt, Bm, Cm, z, {s[0], 0}, {s[1], 0}, {s[2], 0}, {s[3], 0}, {s[4], 0},
+                       A, D_skip, dt_bias, nullptr, nullptr, y, h, B, 1, D, G, N, dt_softplus != 0,
+                       dtype == GDR_BF16, nullptr};
+    int launches = 0;
+    const cudaError_t e = gdr::launch_ssm_scan_step(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
 }

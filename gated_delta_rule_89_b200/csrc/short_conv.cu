@@ -1,0 +1,448 @@
+// Short causal depthwise convolution with an optional SiLU, in front of a
+// token mixer: prompt, backward and single token.
+//
+//   pre[t, c] = bias[c] + sum_{j<W} weight[c, j] x[t - (W-1) + j, c],   y = pre or pre * sigmoid(pre)
+//
+// where the W-1 rows before a sequence are its carried state.  ("Token Mixer
+// I", section "The Kimi Linear Model Architecture": q, k and v are
+// Swish(ShortConv(W x)).)  Channels are independent and tokens touch only
+// their W-1 predecessors, so the work is bound by HBM: each input row is read
+// once and each output row written once.
+//
+// Every thread owns a few neighbouring channels (16 bytes of them where the
+// layout allows) and walks a run of tokens with the last W-1 rows in
+// registers; neighbouring threads own neighbouring channels, so every access
+// of a warp is one contiguous run of a token row.
+#include "ssm_internal.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kSms = 148;
+
+// blockDim.x channel vectors by blockDim.y token runs; grid.x counts (batch,
+// run) pairs, grid.y channel vectors.
+struct ConvGrid {
+    dim3 block, grid;
+    int run, runs;   // tokens of a run, runs of a row
+};
+
+// The run length: long enough that the W-1 rows read again at its start (and,
+// backward, at its end) cost little, short enough that small problems still
+// spread over the machine.
+ConvGrid conv_grid(int B, int T, long long vectors, int threads_per_sm, int longest)
+{
+    ConvGrid g;
+    int bx = 1;
+    while (bx < kConvThreads && bx < vectors) bx *= 2;
+    // whole warps along the channels; drop to 32 where a wider block would idle on the last vectors
+    while (bx > 32 && (vectors + bx - 1) / bx * bx - vectors >= 32) bx /= 2;
+    g.block = dim3(bx, kConvThreads / bx);
+    const long long want = (long long)kSms * threads_per_sm;
+    long long run = ((long long)B * T * vectors + want - 1) / want;
+    run = (run + 7) / 8 * 8;
+    g.run = (int)(run < 8 ? 8 : run > longest ? longest : run);
+    g.runs = T > 0 ? (T + g.run - 1) / g.run : 1;
+    const long long rows = (long long)B * g.runs;
+    g.grid = dim3((unsigned)((rows + g.block.y - 1) / g.block.y), (unsigned)((vectors + bx - 1) / bx));
+    return g;
+}
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int run, int runs)
+{
+    using V = typename Pack<T, VEC>::V;
+    constexpr int U = VEC > 1 ? 8 : 16;   // rows loaded ahead
+    const int D = a.H * a.d;
+    const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const int b = (int)(piece / runs);
+    if (c0 >= D || b >= a.B) return;
+    const int t0 = (int)(piece - (long long)b * runs) * run;
+    const int head = c0 / a.d, j0 = c0 - head * a.d;
+    const int len = row_length(a.lengths, b, a.T);
+
+    const T *x = (const T *)a.x + b * a.xs.b + head * a.xs.h + j0;
+    const T *st = a.state ? (const T *)a.state + (size_t)b * (W - 1) * D + c0 : nullptr;
+
+    // the W-1 rows before the run, oldest first
+    V before[W - 1];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+        const int r = t0 - (W - 1) + i;
+        before[i] = r >= 0 ? (r < len ? *(const V *)(x + r * a.xs.t) : zero_pack<V>())
+                           : (st ? *(const V *)(st + (size_t)(W - 1 + r) * D) : zero_pack<V>());
+    }
+    // The thread of a row's first run also writes its final state.  `before` is
+    // the whole carried state there, in registers, so state_out may be the same
+    // buffer, and a row shorter than W-1 keeps what it has to keep.
+    if (t0 == 0 && a.state_out) {
+        T *so = (T *)a.state_out + (size_t)b * (W - 1) * D + c0;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int r = len - (W - 1) + i;
+            V v = zero_pack<V>();
+            if (r >= 0) v = *(const V *)(x + r * a.xs.t);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+                if (r == k - (W - 1)) v = before[k];
+            *(V *)(so + (size_t)i * D) = v;
+        }
+    }
+    const int t1 = min(t0 + run, len);
+    if (t0 >= t1) return;
+
+    float w[W][VEC], bias[VEC], win[W - 1][VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][v] = a.weight[(size_t)(c0 + v) * W + j];
+        bias[v] = a.bias ? a.bias[c0 + v] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) unpack(before[i], win[i]);
+
+    x += t0 * a.xs.t;
+    T *y = (T *)a.y + (((size_t)b * a.H + head) * a.T + t0) * a.d + j0;
+    for (int t = t0; t < t1; t += U) {
+        V in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) in[u] = t + u < t1 ? *(const V *)(x + u * a.xs.t) : zero_pack<V>();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float cur[VEC], acc[VEC];
+            unpack(in[u], cur);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float s = bias[v];
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) s = fmaf(w[i][v], win[i][v], s);
+                s = fmaf(w[W - 1][v], cur[v], s);
+                acc[v] = a.silu ? s * sigmoid_f32(s) : s;
+#pragma unroll
+                for (int i = 0; i + 1 < W - 1; ++i) win[i][v] = win[i + 1][v];
+                win[W - 2][v] = cur[v];
+            }
+            if (t + u < t1) {
+                V out;
+                pack(out, acc);
+                *(V *)(y + (size_t)u * a.d) = out;
+            }
+        }
+        x += U * a.xs.t;
+        y += (size_t)U * a.d;
+    }
+}
+
+// One token per row: x [B, D] (row stride xs.b), state [B, W-1, D] shifted in place.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a)
+{
+    using V = typename Pack<T, VEC>::V;
+    const int D = a.d;
+    const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    const int b = blockIdx.x * blockDim.y + threadIdx.y;
+    if (c0 >= D || b >= a.B) return;
+    T *st = (T *)a.state_out + (size_t)b * (W - 1) * D + c0;
+    V rows[W];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) rows[i] = *(const V *)(st + (size_t)i * D);
+    rows[W - 1] = *(const V *)((const T *)a.x + b * a.xs.b + c0);
+    float acc[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) acc[v] = a.bias ? a.bias[c0 + v] : 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        float f[VEC];
+        unpack(rows[i], f);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[v] = fmaf(a.weight[(size_t)(c0 + v) * W + i], f[v], acc[v]);
+    }
+    if (a.silu) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[v] *= sigmoid_f32(acc[v]);
+    }
+    V out;
+    pack(out, acc);
+    *(V *)((T *)a.y + (size_t)b * D + c0) = out;
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) *(V *)(st + (size_t)i * D) = rows[i + 1];
+}
+
+// ------------------------------------------------------------- backward
+//
+//   dpre[t] = dy[t] act'(pre[t])   (0 behind the row's end),
+//   dx[r]   = sum_j weight[j] dpre[r + W-1-j],   dweight[j] = sum_t dpre[t] x[t - (W-1) + j],
+//   dbias   = sum_t dpre[t];   rows r < 0 are the gradient of the carried state, and the final
+//   state's gradient adds to the rows it was copied from.
+//
+// One walk forward over a run and W-1 tokens beyond it: at token t the
+// pre-activation is recomputed from the window of x, and row t-(W-1), whose
+// last term that was, is written.  A thread sums dweight and dbias of its run
+// in registers, a block over its runs in shared memory, and the blocks'
+// partial sums are added by a second kernel in a fixed order, so the result
+// does not depend on scheduling.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvBwdArgs a, int run, int runs, float *part)
+{
+    using V = typename Pack<T, VEC>::V;
+    constexpr int U = VEC > 1 ? 4 : 8;
+    const int D = a.H * a.d;
+    const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+    const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const int b = (int)(piece / runs);
+    float dw[W][VEC] = {}, db[VEC] = {};
+
+    if (c0 < D && b < a.B) {
+        const int t0 = (int)(piece - (long long)b * runs) * run;
+        const int head = c0 / a.d, j0 = c0 - head * a.d;
+        const int len = row_length(a.lengths, b, a.T);
+        const int t1 = min(t0 + run, a.T);            // rows [t0, t1) are this run's
+        const bool first = t0 == 0;
+        const T *x = (const T *)a.x + b * a.xs.b + head * a.xs.h + j0;
+        const T *dy = (const T *)a.dy + b * a.dys.b + head * a.dys.h + j0;
+        T *dx = (T *)a.dx + b * a.dxs.b + head * a.dxs.h + j0;
+        const T *st = a.state ? (const T *)a.state + (size_t)b * (W - 1) * D + c0 : nullptr;
+        const T *dso = a.dstate_out ? (const T *)a.dstate_out + (size_t)b * (W - 1) * D + c0 : nullptr;
+        T *dst = a.dstate ? (T *)a.dstate + (size_t)b * (W - 1) * D + c0 : nullptr;
+
+        float w[W][VEC], bias[VEC], win[W - 1][VEC], dp[W][VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                w[j][v] = a.weight[(size_t)(c0 + v) * W + j];
+                dp[j][v] = 0.f;
+            }
+            bias[v] = a.bias ? a.bias[c0 + v] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int r = t0 - (W - 1) + i;
+            V v = r >= 0 ? (r < len ? *(const V *)(x + r * a.xs.t) : zero_pack<V>())
+                         : (st ? *(const V *)(st + (size_t)(W - 1 + r) * D) : zero_pack<V>());
+            unpack(v, win[i]);
+        }
+        // rows the walk completes: [-(W-1), t1) from a row's first run, [t0, t1) from the others
+        const int tend = t1 + (W - 1);
+        for (int t = t0; t < tend; t += U) {
+            V xin[U], gin[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool live = t + u < len && t + u < tend;
+                xin[u] = live ? *(const V *)(x + (t + u) * a.xs.t) : zero_pack<V>();
+                gin[u] = live ? *(const V *)(dy + (t + u) * a.dys.t) : zero_pack<V>();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int tt = t + u;
+                if (tt >= tend) break;
+                const bool mine = tt < t1;
+                float cur[VEC], g[VEC], out[VEC];
+                unpack(xin[u], cur);
+                unpack(gin[u], g);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float s = bias[v];
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) s = fmaf(w[i][v], win[i][v], s);
+                    s = fmaf(w[W - 1][v], cur[v], s);
+                    float p = g[v];
+                    if (a.silu) {
+                        const float q = sigmoid_f32(s);
+                        p *= fmaf(s * q, 1.f - q, q);
+                    }
+                    if (tt >= len) p = 0.f;
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) dp[i][v] = dp[i + 1][v];
+                    dp[W - 1][v] = p;
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < W - 1; ++i) dw[i][v] = fmaf(p, win[i][v], dw[i][v]);
+                        dw[W - 1][v] = fmaf(p, cur[v], dw[W - 1][v]);
+                        db[v] += p;
+                    }
+                    float acc = 0.f;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) acc = fmaf(w[j][v], dp[W - 1 - j][v], acc);
+                    out[v] = acc;
+#pragma unroll
+                    for (int i = 0; i + 1 < W - 1; ++i) win[i][v] = win[i + 1][v];
+                    win[W - 2][v] = cur[v];
+                }
+                const int r = tt - (W - 1);
+                if (r < t0 && !first) continue;
+                if (dso && r >= len - (W - 1) && r < len) {
+                    float f[VEC];
+                    unpack(*(const V *)(dso + (size_t)(r - len + W - 1) * D), f);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) out[v] += f[v];
+                }
+                V o;
+                pack(o, out);
+                if (r >= 0)
+                    *(V *)(dx + r * a.dxs.t) = o;
+                else if (dst)
+                    *(V *)(dst + (size_t)(r + W - 1) * D) = o;
+            }
+        }
+    }
+
+    // the block's runs, added in the order of threadIdx.y
+    __shared__ float sum[kConvThreads][VEC];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sum[tid][v] = j < W ? dw[j < W ? j : 0][v] : db[v];
+        __syncthreads();
+        if (threadIdx.y == 0 && c0 < D) {
+            for (int k = 1; k < (int)blockDim.y; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) sum[tid][v] += sum[tid + k * blockDim.x][v];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) part[((size_t)blockIdx.x * (W + 1) + j) * D + c0 + v] = sum[tid][v];
+        }
+        __syncthreads();
+    }
+}
+
+// Adds the blocks' partial sums [parts][W+1][D]: 32 columns a block, each by
+// 32 threads that take every 32nd partial sum and join in a fixed tree.
+__global__ void __launch_bounds__(1024)
+conv_bwd_sum_kernel(const float *part, int parts, int D, int W, float *dweight, float *dbias)
+{
+    __shared__ float s[32][33];
+    const int n = (W + 1) * D, col = blockIdx.x * 32 + threadIdx.x;
+    float acc = 0.f;
+    if (col < n)
+        for (int p = threadIdx.y; p < parts; p += 32) acc += part[(size_t)p * n + col];
+    s[threadIdx.y][threadIdx.x] = acc;
+    for (int k = 16; k > 0; k >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.y < k) s[threadIdx.y][threadIdx.x] += s[threadIdx.y + k][threadIdx.x];
+    }
+    if (threadIdx.y == 0 && col < n) {
+        const int j = col / D, c = col - j * D;
+        if (j < W) dweight[(size_t)c * W + j] = s[0][threadIdx.x];
+        else if (dbias) dbias[c] = s[0][threadIdx.x];
+    }
+}
+
+// 16-byte accesses need every pointer and every stride to keep 16-byte
+// alignment and the channels of a head to be a whole number of vectors.
+template <typename T> bool conv_vectors(int d, int vec, const void *const *ptrs, int np, const RowStrides *s, int ns)
+{
+    if (d % vec) return false;
+    for (int i = 0; i < np; ++i)
+        if (ptrs[i] && !aligned_to(ptrs[i], vec * sizeof(T))) return false;
+    for (int i = 0; i < ns; ++i)
+        if (s[i].b % vec || s[i].h % vec || s[i].t % vec) return false;
+    return true;
+}
+
+template <typename T, int VEC, int W>
+cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
+{
+    const ConvGrid g = conv_grid(a.B, a.T, (long long)a.H * a.d / VEC, 512, 64);
+    conv_fwd_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a, g.run, g.runs);
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC, int W>
+cudaError_t conv_step(const ConvArgs &a, cudaStream_t st)
+{
+    const ConvGrid g = conv_grid(a.B, 1, a.d / VEC, 512, 8);
+    conv_step_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+constexpr int kBwdLongest = 128;
+ConvGrid conv_bwd_grid(int B, int T, long long vectors) { return conv_grid(B, T, vectors, 512, kBwdLongest); }
+
+template <typename T, int VEC, int W>
+cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
+{
+    const int D = a.H * a.d;
+    const ConvGrid g = conv_bwd_grid(a.B, a.T, D / VEC);
+    conv_bwd_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a, g.run, g.runs, (float *)a.workspace);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    conv_bwd_sum_kernel<<<((W + 1) * D + 31) / 32, dim3(32, 32), 0, st>>>((const float *)a.workspace, (int)g.grid.x,
+                                                                            D, W, a.dweight, a.dbias);
+    return cudaGetLastError();
+}
+
+enum Form { FWD, STEP };
+
+template <typename T, int VEC, Form F>
+cudaError_t by_width(const ConvArgs &a, cudaStream_t st)
+{
+    switch (a.W) {
+        case 2: return F == FWD ? conv_fwd<T, VEC, 2>(a, st) : conv_step<T, VEC, 2>(a, st);
+        case 3: return F == FWD ? conv_fwd<T, VEC, 3>(a, st) : conv_step<T, VEC, 3>(a, st);
+        default: return F == FWD ? conv_fwd<T, VEC, 4>(a, st) : conv_step<T, VEC, 4>(a, st);
+    }
+}
+
+template <Form F>
+cudaError_t by_type(const ConvArgs &a, cudaStream_t st)
+{
+    const void *p[] = {a.x, a.state, a.y, a.state_out};
+    if (a.bf16)
+        return conv_vectors<__nv_bfloat16>(a.d, 8, p, 4, &a.xs, 1) ? by_width<__nv_bfloat16, 8, F>(a, st)
+                                                                   : by_width<__nv_bfloat16, 1, F>(a, st);
+    return conv_vectors<float>(a.d, 4, p, 4, &a.xs, 1) ? by_width<float, 4, F>(a, st) : by_width<float, 1, F>(a, st);
+}
+
+template <typename T, int VEC>
+cudaError_t bwd_by_width(const ConvBwdArgs &a, cudaStream_t st)
+{
+    switch (a.W) {
+        case 2: return conv_bwd<T, VEC, 2>(a, st);
+        case 3: return conv_bwd<T, VEC, 3>(a, st);
+        default: return conv_bwd<T, VEC, 4>(a, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_short_conv_fwd(const ConvArgs &a, cudaStream_t stream, int *launches)
+{
+    cudaError_t e = by_type<FWD>(a, stream);
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+cudaError_t launch_short_conv_step(const ConvArgs &a, cudaStream_t stream, int *launches)
+{
+    cudaError_t e = by_type<STEP>(a, stream);
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+size_t short_conv_bwd_workspace_bytes(int B, int H, int T, int d, int W)
+{
+    // the partial sums of whichever access width the call will take
+    const long long D = (long long)H * d;
+    const unsigned wide = d % 4 == 0 ? conv_bwd_grid(B, T, D / 4).grid.x : 0, narrow = conv_bwd_grid(B, T, D).grid.x;
+    return (size_t)(wide > narrow ? wide : narrow) * (size_t)(W + 1) * (size_t)D * sizeof(float);
+}
+
+cudaError_t launch_short_conv_bwd(const ConvBwdArgs &a, cudaStream_t stream, int *launches)
+{
+    const void *p[] = {a.x, a.dy, a.dx, a.state, a.dstate_out, a.dstate};
+    const RowStrides s[] = {a.xs, a.dys, a.dxs};
+    cudaError_t e;
+    if (a.bf16)
+        e = conv_vectors<__nv_bfloat16>(a.d, 4, p, 6, s, 3) ? bwd_by_width<__nv_bfloat16, 4>(a, stream)
+                                                            : bwd_by_width<__nv_bfloat16, 1>(a, stream);
+    else
+        e = conv_vectors<float>(a.d, 4, p, 6, s, 3) ? bwd_by_width<float, 4>(a, stream)
+                                                    : bwd_by_width<float, 1>(a, stream);
+    if (e == cudaSuccess) *launches += 2;
+    return e;
+}
+
+}  // namespace gdr

@@ -1,0 +1,195 @@
+// Declarations shared by the short causal convolution and the selective state
+// space scan: argument structures (already validated by the C entry points),
+// launchers, and the scalar functions both use.
+#pragma once
+
+#include "gdr_internal.cuh"
+
+namespace gdr {
+
+// Element strides of a [B, H, T, d] tensor whose last dimension is dense.
+struct RowStrides {
+    long long b, h, t;
+};
+
+// Short causal depthwise convolution; D = H * d channels, channel c = h * d + j.
+struct ConvArgs {
+    const void *x;
+    RowStrides xs;
+    const float *weight, *bias;   // [D, W]; [D] or NULL
+    const void *state;            // [B, W-1, D] or NULL (zeros)
+    const int *lengths;           // [B] or NULL (every row has T tokens)
+    void *y, *state_out;          // [B, H, T, d]; [B, W-1, D] or NULL
+    int B, H, T, d, W;
+    bool silu, bf16;
+};
+
+struct ConvBwdArgs {
+    const void *x, *dy;
+    RowStrides xs, dys, dxs;
+    const float *weight, *bias;
+    const void *state, *dstate_out;
+    const int *lengths;
+    void *dx, *dstate;            // dstate [B, W-1, D] or NULL
+    float *dweight, *dbias;       // [D, W]; [D] or NULL
+    int B, H, T, d, W;
+    bool silu, bf16;
+    void *workspace;              // short_conv_bwd_workspace_bytes()
+};
+
+cudaError_t launch_short_conv_fwd(const ConvArgs &a, cudaStream_t stream, int *launches);
+cudaError_t launch_short_conv_step(const ConvArgs &a, cudaStream_t stream, int *launches);
+cudaError_t launch_short_conv_bwd(const ConvBwdArgs &a, cudaStream_t stream, int *launches);
+size_t short_conv_bwd_workspace_bytes(int B, int H, int T, int d, int W);
+
+// Selective state space scan.  x, dt, z, y [B, T, D]; Bm, Cm [B, T, G, N];
+// strides in elements, the last dimension (the last two of Bm and Cm) dense.
+struct BatchToken {
+    long long b, t;
+};
+struct ScanArgs {
+    const void *x, *dt, *Bm, *Cm, *z;             // z NULL: no output gate
+    BatchToken xs, dts, bs, cs, zs;
+    const float *A, *D_skip, *dt_bias, *h0;       // [D, N]; [D] or NULL; [D] or NULL; [B, D, N] or NULL
+    const int *lengths;
+    void *y;                                      // [B, T, D] dense
+    float *h_T;                                   // [B, D, N] or NULL
+    int B, T, D, G, N;
+    bool softplus, bf16;
+    void *workspace;                              // ssm_scan_fwd_workspace_bytes()
+};
+
+cudaError_t launch_ssm_scan_fwd(const ScanArgs &a, cudaStream_t stream, int *launches);
+// one token: x, dt, z, y [B, D], Bm, Cm [B, G, N] (the .t strides unused); h_T is updated in place
+cudaError_t launch_ssm_scan_step(const ScanArgs &a, cudaStream_t stream, int *launches);
+size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N);
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x, from the hardware's approximation: measured over [-16, 0] it is off by
+// at most 1.5e-7 of the value and 5e-8 at the mean, about the rounding of its
+// fp32 result.
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_approx(1.f + exp2_approx(-kLog2e * x)); }
+
+// log(1 + e) for e in [0, 1], as e times a polynomial of degree 9 in e (a
+// weighted least-squares fit to log(1 + e) / e, relative error 5e-9, so the
+// fp32 rounding of its evaluation, 1.6e-7, is what is left).  A logarithm of
+// 1 + e would lose the digits of a small e in the sum; and time steps of 1e-3
+// have an e of 1e-3.  It also spares the special-function pipe one operation.
+__device__ __forceinline__ float log1p_unit(float e)
+{
+    float p = -0.0032440515f;
+    p = fmaf(p, e, 0.01985158f);
+    p = fmaf(p, e, -0.056959756f);
+    p = fmaf(p, e, 0.106036775f);
+    p = fmaf(p, e, -0.15305606f);
+    p = fmaf(p, e, 0.19675943f);
+    p = fmaf(p, e, -0.24954134f);
+    p = fmaf(p, e, 0.33329964f);
+    p = fmaf(p, e, -0.49999902f);
+    p = fmaf(p, e, 1.f);
+    return p * e;
+}
+// log(1 + exp(x)) = max(x, 0) + log(1 + exp(-|x|)); a NaN stays one.
+__device__ __forceinline__ float softplus_f32(float x)
+{
+    return fmaxf(x, 0.f) + log1p_unit(exp2_approx(-kLog2e * fabsf(x)));
+}
+
+// Two fp32 in a 64-bit register pair: one issue slot for two products.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 make_f32x2(float lo, float hi)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo_f32(f32x2 v) { return __uint_as_float((unsigned)v); }
+__device__ __forceinline__ float hi_f32(f32x2 v) { return __uint_as_float((unsigned)(v >> 32)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 exp2_approx2(f32x2 x)
+{
+    return make_f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
+}
+
+// N consecutive elements from / to memory as fp32.  VECTOR: one access of
+// N * sizeof(T) bytes (aligned to that); otherwise one access per element.
+template <typename T, int N> struct Pack;
+template <> struct Pack<float, 4> { using V = float4; };
+template <> struct Pack<__nv_bfloat16, 4> { using V = uint2; };
+template <> struct Pack<__nv_bfloat16, 8> { using V = uint4; };
+template <> struct Pack<float, 1> { using V = float; };
+template <> struct Pack<__nv_bfloat16, 1> { using V = unsigned short; };
+
+// The two bf16 of a 32-bit word are widened by a shift and a mask.
+__device__ __forceinline__ float bf16_lo(unsigned w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ unsigned bf16_pair(float lo, float hi)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&p);
+}
+
+__device__ __forceinline__ void unpack(float4 v, float *f) { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+__device__ __forceinline__ void unpack(uint2 v, float *f)
+{
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+}
+__device__ __forceinline__ void unpack(uint4 v, float *f)
+{
+    unpack(make_uint2(v.x, v.y), f);
+    unpack(make_uint2(v.z, v.w), f + 4);
+}
+__device__ __forceinline__ void unpack(float v, float *f) { f[0] = v; }
+__device__ __forceinline__ void unpack(unsigned short v, float *f) { f[0] = bf16_lo(v); }
+__device__ __forceinline__ void pack(float4 &v, const float *f) { v = make_float4(f[0], f[1], f[2], f[3]); }
+__device__ __forceinline__ void pack(uint2 &v, const float *f)
+{
+    v = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
+}
+__device__ __forceinline__ void pack(uint4 &v, const float *f)
+{
+    v = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+__device__ __forceinline__ void pack(float &v, const float *f) { v = f[0]; }
+__device__ __forceinline__ void pack(unsigned short &v, const float *f) { v = (unsigned short)bf16_pair(f[0], 0.f); }
+
+template <typename V> __device__ __forceinline__ V zero_pack();
+template <> __device__ __forceinline__ float4 zero_pack<float4>() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+template <> __device__ __forceinline__ uint2 zero_pack<uint2>() { return make_uint2(0u, 0u); }
+template <> __device__ __forceinline__ uint4 zero_pack<uint4>() { return make_uint4(0u, 0u, 0u, 0u); }
+template <> __device__ __forceinline__ float zero_pack<float>() { return 0.f; }
+template <> __device__ __forceinline__ unsigned short zero_pack<unsigned short>() { return 0; }
+
+// The number of tokens of row b: T, or lengths[b] brought into [0, T].
+__device__ __forceinline__ int row_length(const int *lengths, int b, int T)
+{
+    return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+}  // namespace gdr

@@ -294,6 +294,113 @@ int gdr_chunk_fwd_noalloc(const void *q, const void *k, const void *v, const flo
                           void *stream);
 
 /*
+ * Short causal depthwise convolution with an optional SiLU: what a layer puts
+ * in front of q, k and v ("Token Mixer I", section "The Kimi Linear Model
+ * Architecture": Swish(ShortConv(W x))) or of a state space scan.  Channel
+ * c = h d + j of the D = H d channels:
+ *     pre[t,c] = bias[c] + sum_{j<W} weight[c,j] x[t - (W-1) + j, c],
+ *     y        = pre                 (GDR_ACT_NONE)
+ *              = pre sigmoid(pre)    (GDR_ACT_SILU)
+ * with the W-1 rows before the sequence taken from `state`.  Products and
+ * sums are fp32, rounded once on the way out.
+ *
+ *   x         [B,H,T,d]   dtype     input; x_strides = {batch, head, token} in
+ *                                   elements (>= 0; the last dimension is
+ *                                   dense), NULL = dense.  A projection's
+ *                                   rows [B,T,H*d] are {T*H*d, d, H*d}
+ *   weight    [D,W]       float     W in {2, 3, 4}; weight[c,W-1] multiplies
+ *                                   the current token
+ *   bias      [D]         float     NULL = none
+ *   state     [B,W-1,D]   dtype     the rows before the sequence, oldest
+ *                                   first; NULL = zeros
+ *   lengths   [B]         int       tokens of each row, taken into [0,T]; NULL
+ *                                   = T.  What lies behind a row's end is not
+ *                                   read, and y is left as it was there
+ *   y         [B,H,T,d]   dtype     output (written, dense)
+ *   state_out [B,W-1,D]   dtype     the last W-1 rows of (state, x) (written);
+ *                                   NULL = not wanted; may be `state` itself
+ * The convolution and scan calls need their dtype tensors aligned to one
+ * element only, float and int vectors to 4 bytes; they take 16-byte (8-byte)
+ * accesses where pointers and strides allow it, one element at a time
+ * otherwise.  B and D <= 2^20, T < 2^30, B T D < 2^40.
+ */
+typedef enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
+
+int gdr_short_conv_fwd(const void *x, const float *weight, const float *bias, const void *state,
+                       const int *lengths, void *y, void *state_out, const long long *x_strides,
+                       int B, int H, int T, int d, int W, int act, int dtype, void *stream);
+
+/*
+ * The same for one token per row: x, y [B,D] (x_stride elements between rows
+ * of x), state [B,W-1,D] dtype, shifted by the token IN PLACE.
+ */
+int gdr_short_conv_step(const void *x, const float *weight, const float *bias, void *state, void *y,
+                        long long x_stride, int B, int D, int W, int act, int dtype, void *stream);
+
+/*
+ * Backward of gdr_short_conv_fwd: the gradients of <dy, y> + <dstate_out,
+ * state_out> with respect to x, weight, bias and state; the pre-activations
+ * are recomputed.  dy and dx [B,H,T,d] have strides of their own (as
+ * x_strides; those of dx must not make rows overlap); dx is zero behind a
+ * row's end, where dy is not read.  dstate_out NULL = zeros; dbias and dstate
+ * NULL = not wanted.  dweight and dbias are summed in fp32 in a fixed order:
+ * equal calls give equal bits.  The workspace (device, 16-byte aligned) holds
+ * the partial sums.
+ */
+size_t gdr_short_conv_bwd_workspace_size(int B, int H, int T, int d, int W, int dtype);
+
+int gdr_short_conv_bwd(const void *x, const float *weight, const float *bias, const void *state,
+                       const int *lengths, const void *dy, const void *dstate_out,
+                       void *dx, float *dweight, float *dbias, void *dstate,
+                       const long long *x_strides, const long long *dy_strides, const long long *dx_strides,
+                       int B, int H, int T, int d, int W, int act, int dtype,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Selective state space scan: the diagonal relative of the gated delta rule
+ * (a decay of its own per channel and state, no delta term; "Token Mixer I",
+ * section "Mamba2: Linear Attention with Decay", is its scalar case).  For
+ * channel d of group g = d / (D/G) and states n < N:
+ *     delta_t = dt_t[d] + dt_bias[d], through log(1 + exp(.)) if dt_softplus
+ *     h_t[n]  = exp(delta_t A[d,n]) h_{t-1}[n] + delta_t x_t[d] Bm_t[g,n]
+ *     y_t[d]  = (sum_n Cm_t[g,n] h_t[n] + D_skip[d] x_t[d]) silu(z_t[d])
+ * States, time steps and sums are fp32; y is rounded once.
+ *
+ *   x, dt, z [B,T,D]     dtype     z NULL = no output gate
+ *   Bm, Cm   [B,T,G,N]   dtype     shared by the D/G channels of a group; D % G == 0
+ *   A        [D,N]       float     N in {8, 16, 32, 64}
+ *   D_skip, dt_bias [D]  float     NULL = none
+ *   h0       [B,D,N]     float     state before the sequence; NULL = zeros
+ *   lengths  [B]         int       as gdr_short_conv_fwd
+ *   y        [B,T,D]     dtype     output (written, dense)
+ *   h_T      [B,D,N]     float     state after each row's last token
+ *                                  (written); NULL = not wanted; may be h0
+ *   strides                        {batch, token} strides, in elements, of x,
+ *                                  dt, Bm, Cm, z in that order (10 values >=
+ *                                  0; the rest is dense); NULL = all dense
+ * A, h0, h_T and the workspace must be 16-byte aligned.  The workspace (0
+ * bytes for most sizes) holds the states between the pieces that a row is cut
+ * into when there are few channels.
+ */
+size_t gdr_ssm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dtype);
+
+int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                     const float *D_skip, const void *z, const float *dt_bias, const float *h0,
+                     const int *lengths, void *y, float *h_T, const long long *strides,
+                     int B, int T, int D, int G, int N, int dt_softplus, int dtype,
+                     void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One token of the scan per row: x, dt, z, y [B,D], Bm, Cm [B,G,N], h [B,D,N]
+ * float updated IN PLACE; strides = the row strides of x, dt, Bm, Cm, z (5
+ * values; NULL = dense).
+ */
+int gdr_ssm_scan_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                      const float *D_skip, const void *z, const float *dt_bias, float *h, void *y,
+                      const long long *strides, int B, int D, int G, int N, int dt_softplus, int dtype,
+                      void *stream);
+
+/*
  * Device-side status.  Kernels that wait on other warps of their own block
  * bound every wait (about a second); when one runs out the kernel records
  * GDR_ERR_TIMEOUT in a device status word, stops, and leaves its outputs
