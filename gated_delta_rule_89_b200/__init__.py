@@ -22,7 +22,7 @@ import torch
 __all__ = ["chunk_fwd", "recurrent_step", "chunk_fwd_workspace_size", "chunk_fwd_prologue", "chunk_fwd_gdr2",
            "chunk_fwd_gated", "chunk_bwd",
            "recurrent_step_gdr2", "short_conv_fwd", "short_conv_step", "short_conv_bwd", "ssm_scan_fwd",
-           "ssm_scan_step", "ssm_scan_fwd_workspace_size", "GDRError", "library_path",
+           "ssm_scan_step", "ssm_scan_bwd", "ssm_scan_fwd_workspace_size", "ssm_scan_bwd_workspace_size", "GDRError", "library_path",
            "last_launch_count", "device_status", "GATE_PER_CHANNEL", "GATE_SCALAR"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -82,6 +82,9 @@ def lib() -> ctypes.CDLL:
         L.gdr_ssm_scan_fwd.argtypes = [P] * 13 + [I] * 7 + [P, Z, P]
         L.gdr_ssm_scan_fwd_workspace_size.argtypes = [I] * 6
         L.gdr_ssm_scan_fwd_workspace_size.restype = Z
+        L.gdr_ssm_scan_bwd.argtypes = [P] * 22 + [I] * 7 + [P, Z, P]
+        L.gdr_ssm_scan_bwd_workspace_size.argtypes = [I] * 6
+        L.gdr_ssm_scan_bwd_workspace_size.restype = Z
         L.gdr_ssm_scan_step.argtypes = [P] * 11 + [I] * 6 + [P]
         L.gdr_status_string.argtypes = [I]
         L.gdr_status_string.restype = ctypes.c_char_p
@@ -526,5 +529,5 @@ def chunk_bwd_workspace_size(B, H, T, dk, dv, C=64, gate="per_channel", dtype=to
     return int(lib().gdr_chunk_bwd_workspace_size(B, H, T, dk, dv, C, g, _DTYPES[dtype]))
 
 
-from .ssm import (short_conv_bwd, short_conv_fwd, short_conv_step, ssm_scan_fwd,   # noqa: E402
-                  ssm_scan_fwd_workspace_size, ssm_scan_step)
+from .ssm import (short_conv_bwd, short_conv_fwd, short_conv_step, ssm_scan_bwd,   # noqa: E402
+                  ssm_scan_bwd_workspace_size, ssm_scan_fwd, ssm_scan_fwd_workspace_size, ssm_scan_step)

@@ -627,3 +627,49 @@ GDR_API int gdr_ssm_scan_step(const void *x, const void *dt, const float *A, con
     const cudaError_t e = gdr::launch_ssm_scan_step(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
 }
+
+GDR_API size_t gdr_ssm_scan_bwd_workspace_size(int B, int T, int D, int G, int N, int dtype)
+{
+    if (scan_sizes(B, T, D, G, N, dtype) || B == 0 || D == 0) return 0;
+    if ((long long)B * (T ? T : 1) * G * N >= (1LL << 38)) return 0;
+    return gdr::ssm_scan_bwd_workspace_bytes(B, T, D, G, N);
+}
+
+GDR_API int gdr_ssm_scan_bwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                             const float *D_skip, const void *z, const float *dt_bias, const float *h0,
+                             const int *lengths, const void *dy, const float *dh_T,
+                             void *dx, void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias,
+                             float *dh0, const long long *strides, int B, int T, int D, int G, int N, int dt_softplus,
+                             int dtype, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (const int e = scan_sizes(B, T, D, G, N, dtype)) return e;
+    if ((long long)B * (T ? T : 1) * G * N >= (1LL << 38)) return GDR_ERR_UNSUPPORTED;
+    if (any_negative(strides, 12)) return GDR_ERR_INVALID_ARG;
+    if (D == 0) return nothing_to_do();
+    const void *need[] = {x, dt, Bm, Cm, dy, dx, ddt, dB, dC};
+    if (!A || !dA || (z && B > 0 && T > 0 && !dz) || (B > 0 && T > 0 && any_null(need, 9))) return GDR_ERR_INVALID_ARG;
+    const void *rows[] = {x, dt, Bm, Cm, z, dy, dx, ddt, dB, dC, dz};
+    const void *words[] = {D_skip, dt_bias, lengths, dD, ddt_bias}, *lines[] = {A, h0, dh_T, dA, dh0, workspace};
+    if (any_misaligned(rows, 11, elem_bytes(dtype)) || any_misaligned(words, 5, 4) || any_misaligned(lines, 6, 16))
+        return GDR_ERR_ALIGNMENT;
+    const size_t ws_need = gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N, dtype);
+    if (ws_bytes < ws_need || (ws_need && !workspace)) return GDR_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (B == 0) {   // the sums over no rows
+        cudaError_t e = cudaMemsetAsync(dA, 0, sizeof(float) * (size_t)D * N, st);
+        if (e == cudaSuccess && dD) e = cudaMemsetAsync(dD, 0, sizeof(float) * (size_t)D, st);
+        if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, sizeof(float) * (size_t)D, st);
+        return finish(e, 0);
+    }
+    const long long *s = strides;
+    gdr::ScanBwdArgs a = {
+        {x, dt, Bm, Cm, z, tokens_or_dense(s, T, D), tokens_or_dense(s ? s + 2 : s, T, D),
+         tokens_or_dense(s ? s + 4 : s, T, (long long)G * N), tokens_or_dense(s ? s + 6 : s, T, (long long)G * N),
+         tokens_or_dense(s ? s + 8 : s, T, D), A, D_skip, dt_bias, h0, lengths, nullptr, nullptr, B, T, D, G, N,
+         dt_softplus != 0, dtype == GDR_BF16, nullptr},
+        dy, tokens_or_dense(s ? s + 10 : s, T, D), dh_T, dx, ddt, dB, dC, z ? dz : nullptr, dA, dD, ddt_bias, dh0,
+        workspace};
+    int launches = 0;
+    const cudaError_t e = gdr::launch_ssm_scan_bwd(a, st, &launches);
+    return finish(e, launches);
+}

@@ -64,6 +64,25 @@ cudaError_t launch_ssm_scan_fwd(const ScanArgs &a, cudaStream_t stream, int *lau
 cudaError_t launch_ssm_scan_step(const ScanArgs &a, cudaStream_t stream, int *launches);
 size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N);
 
+// The states ahead of every kCheckpoint-th token: [B][ceil(T / kCheckpoint)][D][N]
+// (those of tokens that a row does not have are not written).  Only the inputs
+// of the recurrence are read (x, dt, Bm, A, dt_bias, h0); a.workspace as for
+// launch_ssm_scan_fwd.
+constexpr int kCheckpoint = 8;
+cudaError_t launch_ssm_scan_checkpoints(const ScanArgs &a, float *states, cudaStream_t stream, int *launches);
+
+struct ScanBwdArgs {
+    ScanArgs f;                                   // the forward's inputs (y, h_T unused)
+    const void *dy;
+    BatchToken dys;
+    const float *dh_T;                            // [B, D, N] or NULL
+    void *dx, *ddt, *dB, *dC, *dz;                // dense; dz NULL without a gate
+    float *dA, *dD, *ddt_bias, *dh0;              // dD, ddt_bias, dh0 may be NULL
+    void *workspace;                              // ssm_scan_bwd_workspace_bytes()
+};
+cudaError_t launch_ssm_scan_bwd(const ScanBwdArgs &a, cudaStream_t stream, int *launches);
+size_t ssm_scan_bwd_workspace_bytes(int B, int T, int D, int G, int N);
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 2^x, from the hardware's approximation: measured over [-16, 0] it is off by
@@ -188,6 +207,41 @@ template <> __device__ __forceinline__ unsigned short zero_pack<unsigned short>(
 __device__ __forceinline__ int row_length(const int *lengths, int b, int T)
 {
     return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+// 4 consecutive elements, of which the first `valid` exist (the rest are 0).
+// VECTOR: groups are whole and aligned, so valid is <= 0 or >= 4.
+template <typename T, bool VECTOR>
+__device__ __forceinline__ typename Pack<T, 4>::V load4(const T *p, int valid)
+{
+    using V = typename Pack<T, 4>::V;
+    V v = zero_pack<V>();
+    if (VECTOR) {
+        if (valid > 0) v = *(const V *)p;
+    } else {
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < valid) f[k] = to_f32<T>(p[k]);
+        pack(v, f);
+    }
+    return v;
+}
+template <typename T, bool VECTOR>
+__device__ __forceinline__ void store4(T *p, const float *f, int valid)
+{
+    using V = typename Pack<T, 4>::V;
+    if (VECTOR) {
+        if (valid > 0) {
+            V v;
+            pack(v, f);
+            *(V *)p = v;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < valid) p[k] = from_f32<T>(f[k]);
+    }
 }
 
 inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }

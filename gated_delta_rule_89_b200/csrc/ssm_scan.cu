@@ -49,7 +49,8 @@ __device__ __forceinline__ int swz(int chunk) { return chunk ^ ((chunk >> 3) & 3
 
 enum Mode {
     FULL,    // the outputs and the final state
-    LOCAL    // the state that a piece of a row ends with when it starts from zero
+    LOCAL,   // the state that a piece of a row ends with when it starts from zero
+    POINTS   // the states ahead of every kCheckpoint-th token, for the backward
 };
 
 // pieces of a row (time is split when there are few channels), tokens of a
@@ -59,6 +60,7 @@ enum Mode {
 struct Pieces {
     int count, tokens;
     float *slots, *sums;
+    float *points;   // POINTS: [B][ceil(T / kCheckpoint)][D][N]
 };
 
 template <typename T, int N, bool VECTOR, Mode MODE>
@@ -108,7 +110,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             }
         }
         f32x2 h0 = make_f32x2(h.x, h.y), h1 = make_f32x2(h.z, h.w);
-        if (MODE == FULL && on)
+        if (MODE != LOCAL && on)
             for (int s = 1; s <= piece; ++s) {   // fold in the pieces ahead
                 const float sum = pc.sums[((size_t)s * a.B + b) * a.D + c];
                 const float4 q = *(const float4 *)(pc.slots + s * slot + at);
@@ -117,6 +119,9 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 h1 = fma2(exp2_approx2(mul2(ss, A1)), h1, make_f32x2(q.z, q.w));
             }
         float sum = 0.f;
+        float *points = nullptr;
+        if (MODE == POINTS)
+            points = pc.points + (((size_t)b * ((a.T + kCheckpoint - 1) / kCheckpoint) + t0 / kCheckpoint) * a.D + c) * N + n0;
         __syncthreads();
         for (int i = 0; i < tiles; ++i) {
             const float *buf = sm + (i & 1) * S::BUF;
@@ -124,6 +129,8 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             float *py = sm + (i & 1) * S::BUF + S::P + 2 * S::S + swz(tid >> 2) * 4 + (tid & 3);
 #pragma unroll 8
             for (int t = 0; t < kTile; ++t) {
+                if (MODE == POINTS && t % kCheckpoint == 0 && on && t0 + i * kTile + t < t1)
+                    *(ulonglong2 *)(points + (size_t)(i * kTile + t) / kCheckpoint * a.D * N) = make_ulonglong2(h0, h1);
                 const ulonglong2 du = *(const ulonglong2 *)(p + t * S::CB * 4);
                 const ulonglong2 bb = *(const ulonglong2 *)(sb + t * N);
                 const f32x2 a0 = exp2_approx2(mul2(du.x, A0)), a1 = exp2_approx2(mul2(du.x, A1));
@@ -133,7 +140,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                     const ulonglong2 cc = *(const ulonglong2 *)(sc + t * N);
                     const f32x2 y = fma2(h1, cc.y, mul2(h0, cc.x));
                     py[t * kScanLanes] = lo_f32(y) + hi_f32(y);
-                } else {
+                } else if (MODE == LOCAL) {
                     sum += lo_f32(du.x);
                 }
             }
@@ -163,19 +170,6 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             skip[v] = MODE == FULL && a.D_skip && c + v < cend ? a.D_skip[c + v] : 0.f;
         }
 
-        auto load4 = [](const T *p, int valid) -> V {          // `valid` of 4 elements, the rest 0
-            V v = zero_pack<V>();
-            if (VECTOR) {
-                if (valid > 0) v = *(const V *)p;              // groups are whole: valid is <= 0 or >= 4
-            } else {
-                float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < valid) f[k] = to_f32<T>(p[k]);
-                pack(v, f);
-            }
-            return v;
-        };
         V rx[S::R], rdt[S::R], rB[S::RB], rC[S::RB], ex[S::R], ez[S::R];
         auto fetch = [&](int tile) {
             const int tb = t0 + tile * kTile;
@@ -184,16 +178,16 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 const int k = tok + r * S::TPP;
                 const long long t = tb + k;
                 const int valid = k < kTile && t < t1 ? cend - c : 0;
-                rx[r] = load4(px + t * a.xs.t, valid);
-                rdt[r] = load4(pdt + t * a.dts.t, valid);
+                rx[r] = load4<T, VECTOR>(px + t * a.xs.t, valid);
+                rdt[r] = load4<T, VECTOR>(pdt + t * a.dts.t, valid);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
                 const long long t = tb + k;
                 const int valid = k < kTile && t < t1 ? 4 : 0;
-                rB[r] = load4(pB + t * a.bs.t, valid);
-                if (MODE == FULL) rC[r] = load4(pC + t * a.cs.t, valid);
+                rB[r] = load4<T, VECTOR>(pB + t * a.bs.t, valid);
+                if (MODE == FULL) rC[r] = load4<T, VECTOR>(pC + t * a.cs.t, valid);
             }
         };
         auto fetch_out = [&](int tile) {
@@ -202,8 +196,8 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 const int k = tok + r * S::TPP;
                 const long long t = t0 + tile * kTile + k;
                 const int valid = k < kTile && t < t1 ? cend - c : 0;
-                if (a.D_skip) ex[r] = load4(px + t * a.xs.t, valid);
-                if (pz) ez[r] = load4(pz + t * a.zs.t, valid);
+                if (a.D_skip) ex[r] = load4<T, VECTOR>(px + t * a.xs.t, valid);
+                if (pz) ez[r] = load4<T, VECTOR>(pz + t * a.zs.t, valid);
             }
         };
         auto prepare = [&](int tile) {
@@ -262,17 +256,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                     if (pz) s *= fz[v] * sigmoid_f32(fz[v]);
                     out[v] = s;
                 }
-                if (VECTOR) {
-                    if (c < cend) {
-                        V o;
-                        pack(o, out);
-                        *(V *)(py + t * a.D) = o;
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (c + v < cend) py[t * a.D + v] = from_f32<T>(out[v]);
-                }
+                store4<T, VECTOR>(py + t * a.D, out, cend - c);
             }
         };
 
@@ -358,7 +342,7 @@ int blocks_per_group(int D, int G, int N)
 // machine down.
 Pieces plan(int B, int T, int D, int G, int N, void *workspace)
 {
-    Pieces p = {1, T, nullptr, nullptr};
+    Pieces p = {1, T, nullptr, nullptr, nullptr};
     const long long blocks = (long long)B * G * blocks_per_group(D, G, N);
     if (blocks > 0 && blocks * 2 <= kSms && T >= 8 * kTile) {
         long long count = 2 * kSms / blocks;
@@ -399,16 +383,17 @@ cudaError_t run_scan(const ScanArgs &a, const Pieces &p, int pieces, cudaStream_
 }
 
 template <typename T, int N, bool VECTOR>
-cudaError_t scan_typed(const ScanArgs &a, cudaStream_t st, int *launches)
+cudaError_t scan_typed(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
 {
-    const Pieces p = plan(a.B, a.T, a.D, a.G, N, a.workspace);
+    Pieces p = plan(a.B, a.T, a.D, a.G, N, a.workspace);
     cudaError_t e = cudaSuccess;
     if (p.count > 1) {
         e = run_scan<T, N, VECTOR, LOCAL>(a, p, p.count - 1, st);
         if (e != cudaSuccess) return e;
         *launches += 1;
     }
-    e = run_scan<T, N, VECTOR, FULL>(a, p, p.count, st);
+    p.points = points;
+    e = points ? run_scan<T, N, VECTOR, POINTS>(a, p, p.count, st) : run_scan<T, N, VECTOR, FULL>(a, p, p.count, st);
     if (e == cudaSuccess) *launches += 1;
     return e;
 }
@@ -422,13 +407,23 @@ cudaError_t step_typed(const ScanArgs &a, cudaStream_t st)
 }
 
 template <int N>
-cudaError_t scan_n(const ScanArgs &a, cudaStream_t st, int *launches)
+cudaError_t scan_n(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
 {
     if (a.bf16)
-        return scan_vectors<__nv_bfloat16>(a) ? scan_typed<__nv_bfloat16, N, true>(a, st, launches)
-                                              : scan_typed<__nv_bfloat16, N, false>(a, st, launches);
-    return scan_vectors<float>(a) ? scan_typed<float, N, true>(a, st, launches)
-                                  : scan_typed<float, N, false>(a, st, launches);
+        return scan_vectors<__nv_bfloat16>(a) ? scan_typed<__nv_bfloat16, N, true>(a, points, st, launches)
+                                              : scan_typed<__nv_bfloat16, N, false>(a, points, st, launches);
+    return scan_vectors<float>(a) ? scan_typed<float, N, true>(a, points, st, launches)
+                                  : scan_typed<float, N, false>(a, points, st, launches);
+}
+
+cudaError_t any_n(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
+{
+    switch (a.N) {
+        case 8: return scan_n<8>(a, points, st, launches);
+        case 16: return scan_n<16>(a, points, st, launches);
+        case 32: return scan_n<32>(a, points, st, launches);
+        default: return scan_n<64>(a, points, st, launches);
+    }
 }
 
 }  // namespace
@@ -441,12 +436,12 @@ size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N)
 
 cudaError_t launch_ssm_scan_fwd(const ScanArgs &a, cudaStream_t stream, int *launches)
 {
-    switch (a.N) {
-        case 8: return scan_n<8>(a, stream, launches);
-        case 16: return scan_n<16>(a, stream, launches);
-        case 32: return scan_n<32>(a, stream, launches);
-        default: return scan_n<64>(a, stream, launches);
-    }
+    return any_n(a, nullptr, stream, launches);
+}
+
+cudaError_t launch_ssm_scan_checkpoints(const ScanArgs &a, float *states, cudaStream_t stream, int *launches)
+{
+    return any_n(a, states, stream, launches);
 }
 
 cudaError_t launch_ssm_scan_step(const ScanArgs &a, cudaStream_t stream, int *launches)

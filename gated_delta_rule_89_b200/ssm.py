@@ -25,7 +25,7 @@ _ACTIVATIONS = {None: 0, "silu": 1}
 _I64x3 = ctypes.c_longlong * 3
 _I64x5 = ctypes.c_longlong * 5
 _I64x10 = ctypes.c_longlong * 10
-
+_I64x12 = ctypes.c_longlong * 12
 
 
 def _scoped(dev: torch.device, stream, body):
@@ -356,3 +356,54 @@ def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.
         return y
 
     return _scoped(dev, stream, body)
+
+
+def ssm_scan_bwd_workspace_size(B, T, D, G=1, N=16, dtype=torch.bfloat16) -> int:
+    return int(lib().gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N, _DTYPES[dtype]))
+
+
+def ssm_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                 dy: torch.Tensor, D_skip: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                 dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                 h0: Optional[torch.Tensor] = None, dh_T: Optional[torch.Tensor] = None,
+                 lengths: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of ``ssm_scan_fwd`` (``gdr_ssm_scan_bwd``): the gradients of <dy, y> + <dh_T, h_T>.
+
+    Inputs as ``ssm_scan_fwd``, dy [B,T,D] in x's type (strided), dh_T [B,D,N] fp32 or None.
+    Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0), each in its input's shape and type
+    (contiguous) and None where that input is; dx, ddt, dB, dC and dz are zero behind a row's end.
+    """
+    ty = _type_of(x)
+    dev, host = _device(x), not x.is_cuda
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,D]")
+    B, T, D = x.shape
+
+    def body(handle, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, dy=dy, D_skip=D_skip, z=z, dt_bias=dt_bias, h0=h0, dh_T=dh_T,
+             lengths=lengths):
+        if host:
+            x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, h0, dh_T, lengths = (
+                _to_device(t, dev) for t in (x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, h0, dh_T, lengths))
+        G, N = _scan_inputs(x, dt, A, Bm, Cm, D_skip, z, dt_bias, (B, T), dev)
+        _rows(dy, "dy", x.shape, ty, dev)
+        _vector(h0, "h0", (B, D, N), dev)
+        _vector(dh_T, "dh_T", (B, D, N), dev)
+        _vector(lengths, "lengths", (B,), dev, torch.int32)
+
+        def like(t, *shape, dtype=torch.float32):
+            return None if t is None else torch.empty(shape, dtype=dtype, device=dev)
+        dx, ddt, dz = (like(t, B, T, D, dtype=ty) for t in (x, dt, z))
+        dB, dC = (like(t, B, T, G, N, dtype=ty) for t in (Bm, Cm))
+        dA, dD, db, dh0 = like(A, D, N), like(D_skip, D), like(dt_bias, D), like(h0, B, D, N)
+        L = lib()
+        size = L.gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N, _DTYPES[ty])
+        ws = _workspace(workspace, size, dev)
+        _check(L.gdr_ssm_scan_bwd(
+            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D_skip), _ptr(z), _ptr(dt_bias), _ptr(h0),
+            _ptr(lengths), _ptr(dy), _ptr(dh_T), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dz),
+            _ptr(db), _ptr(dh0), _I64x12(*_scan_strides(x, dt, Bm, Cm, z, dy)), B, T, D, G, N,
+            1 if dt_softplus else 0, _DTYPES[ty], _ptr(ws), size, handle), "gdr_ssm_scan_bwd")
+        return dx, ddt, dA, dB, dC, dD, dz, db, dh0
+
+    out = _scoped(dev, stream, body)
+    return tuple(_to_host(t) for t in out) if host else out

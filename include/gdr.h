@@ -391,6 +391,36 @@ int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *
                      void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * Backward of gdr_ssm_scan_fwd: the gradients of <dy, y> + <dh_T, h_T> with
+ * respect to every input.  The states are recomputed from ones stored every 8
+ * tokens in the workspace (device, 16-byte aligned; N/2 bytes per token and
+ * channel, and the parts of dB and dC).  Arithmetic is fp32, sums go in a
+ * fixed order: equal calls give equal bits.
+ *
+ *   x .. lengths                        as gdr_ssm_scan_fwd
+ *   dy            [B,T,D]     dtype     gradient of y; not read behind a row's end
+ *   dh_T          [B,D,N]     float     gradient of h_T; NULL = zeros
+ *   dx, ddt, dz   [B,T,D]     dtype     (written, dense; zero behind a row's
+ *                                       end); dz unused without z
+ *   dB, dC        [B,T,G,N]   dtype     (written, dense), summed over the
+ *                                       group's channels in fp32
+ *   dA            [D,N]       float     (written)
+ *   dD, ddt_bias  [D]         float     (written); NULL = not wanted
+ *   dh0           [B,D,N]     float     (written); NULL = not wanted
+ *   strides                             as gdr_ssm_scan_fwd with dy's pair
+ *                                       behind the others: 12 values
+ * dA, dh_T and dh0 must be 16-byte aligned.  B T G N < 2^38.
+ */
+size_t gdr_ssm_scan_bwd_workspace_size(int B, int T, int D, int G, int N, int dtype);
+
+int gdr_ssm_scan_bwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                     const float *D_skip, const void *z, const float *dt_bias, const float *h0,
+                     const int *lengths, const void *dy, const float *dh_T,
+                     void *dx, void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias,
+                     float *dh0, const long long *strides, int B, int T, int D, int G, int N, int dt_softplus,
+                     int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * One token of the scan per row: x, dt, z, y [B,D], Bm, Cm [B,G,N], h [B,D,N]
  * float updated IN PLACE; strides = the row strides of x, dt, Bm, Cm, z (5
  * values; NULL = dense).

@@ -96,6 +96,29 @@ def test_scan_step_arguments(L):
     assert step(B=0) == OK and step(D=0) == OK
 
 
+def test_scan_bwd_arguments(L):
+    def bwd(x=GOOD, A=GOOD, z=None, dy=GOOD, dx=GOOD, dA=GOOD, dB=GOOD, dD=None, dz=None, dh0=None, strides=None, B=1,
+            T=4, D=8, G=1, N=16, dtype=1, ws=GOOD, size=1 << 40):
+        return L.gdr_ssm_scan_bwd(x, GOOD, A, GOOD, GOOD, None, z, None, None, None, dy, None, dx, GOOD, dA, dB, GOOD,
+                                  dD, dz, None, dh0, strides, B, T, D, G, N, 1, dtype, ws, size, None)
+    for bad in (dict(B=-1), dict(G=0), dict(x=None), dict(A=None), dict(dy=None), dict(dx=None), dict(dA=None),
+                dict(dB=None), dict(z=GOOD), dict(ws=None), dict(size=0), dict(dtype=4),
+                dict(strides=longs(*[0] * 11, -1))):
+        assert bwd(**bad) == INVALID, bad
+    assert bwd(N=20) == UNSUPPORTED
+    assert bwd(B=1 << 19, T=1 << 14, D=32, G=32, N=64) == UNSUPPORTED
+    for bad in (dict(A=P(0x100008)), dict(dA=P(0x100008)), dict(dh0=P(0x100004)), dict(dD=P(0x100002)),
+                dict(dx=P(0x100001)), dict(ws=P(0x100008))):
+        assert bwd(**bad) == ALIGN, bad
+    need = L.gdr_ssm_scan_bwd_workspace_size(2, 100, 64, 1, 16, 1)
+    # states every 8 tokens, the one block's parts of dB and dC, dA, dD and ddt_bias per row, and
+    # what the forward pass wants
+    up = lambda n: (n + 255) // 256 * 256   # noqa: E731
+    assert need == up(2 * 13 * 64 * 16 * 4) + up(2 * 100 * 32 * 4) + up(2 * 64 * 16 * 4) + up(2 * 64 * 2 * 4) + \
+        L.gdr_ssm_scan_fwd_workspace_size(2, 100, 64, 1, 16, 1)
+    assert bwd(D=0) == OK
+
+
 def test_binding_refuses():
     x = torch.zeros(2, 4, 8)
     with pytest.raises(TypeError):
