@@ -102,31 +102,6 @@ __device__ __forceinline__ float rcp_approx(float x)
 }
 __device__ __forceinline__ float sigmoid_f32(float x) { return rcp_approx(1.f + exp2_approx(-kLog2e * x)); }
 
-// log(1 + e) for e in [0, 1], as e times a polynomial of degree 9 in e (a
-// weighted least-squares fit to log(1 + e) / e, relative error 5e-9, so the
-// fp32 rounding of its evaluation, 1.6e-7, is what is left).  A logarithm of
-// 1 + e would lose the digits of a small e in the sum; and time steps of 1e-3
-// have an e of 1e-3.  It also spares the special-function pipe one operation.
-__device__ __forceinline__ float log1p_unit(float e)
-{
-    float p = -0.0032440515f;
-    p = fmaf(p, e, 0.01985158f);
-    p = fmaf(p, e, -0.056959756f);
-    p = fmaf(p, e, 0.106036775f);
-    p = fmaf(p, e, -0.15305606f);
-    p = fmaf(p, e, 0.19675943f);
-    p = fmaf(p, e, -0.24954134f);
-    p = fmaf(p, e, 0.33329964f);
-    p = fmaf(p, e, -0.49999902f);
-    p = fmaf(p, e, 1.f);
-    return p * e;
-}
-// log(1 + exp(x)) = max(x, 0) + log(1 + exp(-|x|)); a NaN stays one.
-__device__ __forceinline__ float softplus_f32(float x)
-{
-    return fmaxf(x, 0.f) + log1p_unit(exp2_approx(-kLog2e * fabsf(x)));
-}
-
 // Two fp32 in a 64-bit register pair: one issue slot for two products.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 make_f32x2(float lo, float hi)
@@ -149,9 +124,52 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return make_f32x2(v, v); }
 __device__ __forceinline__ f32x2 exp2_approx2(f32x2 x)
 {
     return make_f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
+}
+// The decays 2^(delta A2) of two states.  The hardware's 2^x lies below the
+// exact value by 2e-8 at the mean where it is close to 1, and a slowly
+// decaying state multiplies a thousand of them; raising the exponent by 2e-8
+// leaves a mean error under 1e-8 between 2^-16 and 2^-1 (measured), at no
+// cost, and 2^(2e-8) is still exactly 1, so a time step of 0 keeps the state.
+__device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
+{
+    return exp2_approx2(fma2(delta, A2, both(2e-8f)));
+}
+
+// log(1 + e) for e in [0, 1], as e times a polynomial of degree 9 in e (a
+// weighted least-squares fit to log(1 + e) / e, relative error 5e-9, so the
+// fp32 rounding of its evaluation, 1.6e-7, is what is left).  A logarithm of
+// 1 + e would lose the digits of a small e in the sum; and time steps of 1e-3
+// have an e of 1e-3.  It also spares the special-function pipe one operation.
+__device__ __forceinline__ f32x2 log1p_unit2(f32x2 e)
+{
+    f32x2 p = fma2(both(-0.0032440515f), e, both(0.01985158f));
+    p = fma2(p, e, both(-0.056959756f));
+    p = fma2(p, e, both(0.106036775f));
+    p = fma2(p, e, both(-0.15305606f));
+    p = fma2(p, e, both(0.19675943f));
+    p = fma2(p, e, both(-0.24954134f));
+    p = fma2(p, e, both(0.33329964f));
+    p = fma2(p, e, both(-0.49999902f));
+    p = fma2(p, e, both(1.f));
+    return mul2(p, e);
+}
+// log(1 + exp(x)) = max(x, 0) + log(1 + exp(-|x|)) of two values; a NaN stays
+// one.  `e` receives exp(-|x|).
+__device__ __forceinline__ f32x2 softplus2(f32x2 x, f32x2 &e)
+{
+    const float lo = lo_f32(x), hi = hi_f32(x);
+    e = make_f32x2(exp2_approx(-kLog2e * fabsf(lo)), exp2_approx(-kLog2e * fabsf(hi)));
+    return add2(make_f32x2(fmaxf(lo, 0.f), fmaxf(hi, 0.f)), log1p_unit2(e));
 }
 
 // N consecutive elements from / to memory as fp32.  VECTOR: one access of
@@ -217,12 +235,12 @@ __device__ __forceinline__ typename Pack<T, 4>::V load4(const T *p, int valid)
     using V = typename Pack<T, 4>::V;
     V v = zero_pack<V>();
     if (VECTOR) {
-        if (valid > 0) v = *(const V *)p;
+        if (valid > 0) v = __ldg((const V *)p);
     } else {
         float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (k < valid) f[k] = to_f32<T>(p[k]);
+            if (k < valid) f[k] = to_f32<T>(__ldg(p + k));
         pack(v, f);
     }
     return v;

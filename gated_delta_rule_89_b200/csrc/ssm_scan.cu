@@ -115,33 +115,57 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 const float sum = pc.sums[((size_t)s * a.B + b) * a.D + c];
                 const float4 q = *(const float4 *)(pc.slots + s * slot + at);
                 const f32x2 ss = make_f32x2(sum, sum);
-                h0 = fma2(exp2_approx2(mul2(ss, A0)), h0, make_f32x2(q.x, q.y));
-                h1 = fma2(exp2_approx2(mul2(ss, A1)), h1, make_f32x2(q.z, q.w));
+                h0 = fma2(decay2(ss, A0), h0, make_f32x2(q.x, q.y));
+                h1 = fma2(decay2(ss, A1), h1, make_f32x2(q.z, q.w));
             }
         float sum = 0.f;
         float *points = nullptr;
         if (MODE == POINTS)
             points = pc.points + (((size_t)b * ((a.T + kCheckpoint - 1) / kCheckpoint) + t0 / kCheckpoint) * a.D + c) * N + n0;
         __syncthreads();
+        // Four tokens' operands are loaded ahead of the four in work, and ahead of the stores of
+        // their outputs: shared-memory loads are not moved across stores, and a warp that waited
+        // for each token's loads would spend most of its time there.
+        constexpr int G = 4;
+        struct Token {
+            ulonglong2 du, b, c;
+        };
         for (int i = 0; i < tiles; ++i) {
             const float *buf = sm + (i & 1) * S::BUF;
             const float *p = buf + swz(ch) * 4, *sb = buf + S::P + n0, *sc = sb + S::S;
             float *py = sm + (i & 1) * S::BUF + S::P + 2 * S::S + swz(tid >> 2) * 4 + (tid & 3);
-#pragma unroll 8
-            for (int t = 0; t < kTile; ++t) {
+            Token now[G], next[G];
+            auto fetch = [&](Token *k, int t) {
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    k[j].du = *(const ulonglong2 *)(p + (t + j) * S::CB * 4);
+                    k[j].b = *(const ulonglong2 *)(sb + (t + j) * N);
+                    if (MODE == FULL) k[j].c = *(const ulonglong2 *)(sc + (t + j) * N);
+                }
+            };
+            fetch(now, 0);
+#pragma unroll
+            for (int t = 0; t < kTile; t += G) {
                 if (MODE == POINTS && t % kCheckpoint == 0 && on && t0 + i * kTile + t < t1)
                     *(ulonglong2 *)(points + (size_t)(i * kTile + t) / kCheckpoint * a.D * N) = make_ulonglong2(h0, h1);
-                const ulonglong2 du = *(const ulonglong2 *)(p + t * S::CB * 4);
-                const ulonglong2 bb = *(const ulonglong2 *)(sb + t * N);
-                const f32x2 a0 = exp2_approx2(mul2(du.x, A0)), a1 = exp2_approx2(mul2(du.x, A1));
-                h0 = fma2(a0, h0, mul2(du.y, bb.x));
-                h1 = fma2(a1, h1, mul2(du.y, bb.y));
-                if (MODE == FULL) {
-                    const ulonglong2 cc = *(const ulonglong2 *)(sc + t * N);
-                    const f32x2 y = fma2(h1, cc.y, mul2(h0, cc.x));
-                    py[t * kScanLanes] = lo_f32(y) + hi_f32(y);
-                } else if (MODE == LOCAL) {
-                    sum += lo_f32(du.x);
+                if (t + G < kTile) fetch(next, t + G);
+                float y[G];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const Token &k = now[j];
+                    h0 = fma2(decay2(k.du.x, A0), h0, mul2(k.du.y, k.b.x));
+                    h1 = fma2(decay2(k.du.x, A1), h1, mul2(k.du.y, k.b.y));
+                    if (MODE == FULL) {
+                        const f32x2 s = fma2(h1, k.c.y, mul2(h0, k.c.x));
+                        y[j] = lo_f32(s) + hi_f32(s);
+                    } else if (MODE == LOCAL) {
+                        sum += lo_f32(k.du.x);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    if (MODE == FULL) py[(t + j) * kScanLanes] = y[j];
+                    now[j] = next[j];
                 }
             }
             __syncthreads();
@@ -158,72 +182,95 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
         const int gr = ht % S::GR, tok = ht / S::GR;           // 4 channels, token of a pass
         const int grb = ht % S::GRB, tokb = ht / S::GRB;       // 4 states
         const int c = cfirst + gr * 4;
-        const T *px = (const T *)a.x + b * a.xs.b + c, *pdt = (const T *)a.dt + b * a.dts.b + c;
-        const T *pz = a.z ? (const T *)a.z + b * a.zs.b + c : nullptr;
-        const T *pB = (const T *)a.Bm + b * a.bs.b + (size_t)gi * N + grb * 4;
-        const T *pC = (const T *)a.Cm + b * a.cs.b + (size_t)gi * N + grb * 4;
-        T *py = (T *)a.y + (size_t)b * a.T * a.D + c;
-        float bias[4], skip[4];
+        const int have = cend - c;                             // channels of the group that exist
+        // every group of 4 whole: the tiles that lie inside the piece take no bounds checks
+        const bool whole = cfirst + S::CB <= cend;
+        // running pointers to this thread's first element of the tile that is fetched next
+        const long long first = (long long)t0 + tok, firstb = (long long)t0 + tokb;
+        const T *px = (const T *)a.x + b * a.xs.b + c + first * a.xs.t;
+        const T *pdt = (const T *)a.dt + b * a.dts.b + c + first * a.dts.t;
+        const T *pB = (const T *)a.Bm + b * a.bs.b + (size_t)gi * N + grb * 4 + firstb * a.bs.t;
+        const T *pC = (const T *)a.Cm + b * a.cs.b + (size_t)gi * N + grb * 4 + firstb * a.cs.t;
+        const T *pxo = px;                                     // and of the tile that is finished next
+        const T *pzo = a.z ? (const T *)a.z + b * a.zs.b + c + first * a.zs.t : nullptr;
+        T *py = (T *)a.y + ((size_t)b * a.T + first) * a.D + c;
+        f32x2 bias[2], skip[2];
+        {
+            float f[4], g[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            bias[v] = a.dt_bias && c + v < cend ? a.dt_bias[c + v] : 0.f;
-            skip[v] = MODE == FULL && a.D_skip && c + v < cend ? a.D_skip[c + v] : 0.f;
+            for (int v = 0; v < 4; ++v) {
+                f[v] = a.dt_bias && v < have ? a.dt_bias[c + v] : 0.f;
+                g[v] = MODE == FULL && a.D_skip && v < have ? a.D_skip[c + v] : 0.f;
+            }
+            bias[0] = make_f32x2(f[0], f[1]), bias[1] = make_f32x2(f[2], f[3]);
+            skip[0] = make_f32x2(g[0], g[1]), skip[1] = make_f32x2(g[2], g[3]);
         }
 
         V rx[S::R], rdt[S::R], rB[S::RB], rC[S::RB], ex[S::R], ez[S::R];
         auto fetch = [&](int tile) {
             const int tb = t0 + tile * kTile;
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const long long t = tb + k;
-                const int valid = k < kTile && t < t1 ? cend - c : 0;
-                rx[r] = load4<T, VECTOR>(px + t * a.xs.t, valid);
-                rdt[r] = load4<T, VECTOR>(pdt + t * a.dts.t, valid);
+                const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
+                rx[r] = load4<T, VECTOR>(px + r * S::TPP * a.xs.t, valid);
+                rdt[r] = load4<T, VECTOR>(pdt + r * S::TPP * a.dts.t, valid);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
-                const long long t = tb + k;
-                const int valid = k < kTile && t < t1 ? 4 : 0;
-                rB[r] = load4<T, VECTOR>(pB + t * a.bs.t, valid);
-                if (MODE == FULL) rC[r] = load4<T, VECTOR>(pC + t * a.cs.t, valid);
+                const int valid = full && S::TPB <= kTile ? 4 : k < kTile && tb + k < t1 ? 4 : 0;
+                rB[r] = load4<T, VECTOR>(pB + r * S::TPB * a.bs.t, valid);
+                if (MODE == FULL) rC[r] = load4<T, VECTOR>(pC + r * S::TPB * a.cs.t, valid);
             }
+            px += kTile * a.xs.t;
+            pdt += kTile * a.dts.t;
+            pB += kTile * a.bs.t;
+            pC += kTile * a.cs.t;
         };
         auto fetch_out = [&](int tile) {
+            const int tb = t0 + tile * kTile;
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const long long t = t0 + tile * kTile + k;
-                const int valid = k < kTile && t < t1 ? cend - c : 0;
-                if (a.D_skip) ex[r] = load4<T, VECTOR>(px + t * a.xs.t, valid);
-                if (pz) ez[r] = load4<T, VECTOR>(pz + t * a.zs.t, valid);
+                const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
+                if (a.D_skip) ex[r] = load4<T, VECTOR>(pxo + r * S::TPP * a.xs.t, valid);
+                if (pzo) ez[r] = load4<T, VECTOR>(pzo + r * S::TPP * a.zs.t, valid);
             }
+            pxo += kTile * a.xs.t;
+            if (pzo) pzo += kTile * a.zs.t;
         };
         auto prepare = [&](int tile) {
             float *buf = sm + (tile & 1) * S::BUF;
             const int tb = t0 + tile * kTile;
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                if (k >= kTile) continue;
-                const bool live = tb + k < t1;
+                if (S::TPP > kTile && k >= kTile) continue;
                 float fx[4], fd[4];
                 unpack(rx[r], fx);
                 unpack(rdt[r], fd);
+                float *q = buf + k * S::CB * 4;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    float d = fd[v] + bias[v];
-                    if (a.softplus) d = softplus_f32(d);
-                    if (!live || c + v >= cend) d = 0.f;       // the state stands still
-                    const float u = d * fx[v];
-                    *(float4 *)(buf + ((size_t)k * S::CB + swz(gr * 4 + v)) * 4) = make_float4(d, d, u, u);
+                for (int v = 0; v < 4; v += 2) {
+                    f32x2 e, d = add2(make_f32x2(fd[v], fd[v + 1]), bias[v / 2]);
+                    if (a.softplus) d = softplus2(d, e);
+                    if (!full) {                               // the state stands still
+                        const bool live = tb + k < t1;
+                        d = make_f32x2(live && v < have ? lo_f32(d) : 0.f, live && v + 1 < have ? hi_f32(d) : 0.f);
+                    }
+                    const f32x2 u = mul2(d, make_f32x2(fx[v], fx[v + 1]));
+                    *(float4 *)(q + swz(gr * 4 + v) * 4) = make_float4(lo_f32(d), lo_f32(d), lo_f32(u), lo_f32(u));
+                    *(float4 *)(q + swz(gr * 4 + v + 1) * 4) = make_float4(hi_f32(d), hi_f32(d), hi_f32(u), hi_f32(u));
                 }
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
-                if (k >= kTile) continue;
+                if (S::TPB > kTile && k >= kTile) continue;
                 float f[4];
                 unpack(rB[r], f);
                 *(float4 *)(buf + S::P + k * N + grb * 4) = make_float4(f[0], f[1], f[2], f[3]);
@@ -235,11 +282,13 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
         };
         auto finish = [&](int tile) {
             const float *y = sm + (tile & 1) * S::BUF + S::P + 2 * S::S;
+            const int tb = t0 + tile * kTile;
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const long long t = t0 + tile * kTile + k;
-                if (k >= kTile || t >= t1) continue;
+                if (!full && tb + k >= t1) continue;
+                if (S::TPP > kTile && k >= kTile) continue;
                 float part[N];                                  // the LPC partial sums of 4 channels
 #pragma unroll
                 for (int q = 0; q < N / 4; ++q)
@@ -252,12 +301,21 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                     float s = part[v * S::LPC];
 #pragma unroll
                     for (int l = 1; l < S::LPC; ++l) s += part[v * S::LPC + l];
-                    if (a.D_skip) s = fmaf(skip[v], fx[v], s);
-                    if (pz) s *= fz[v] * sigmoid_f32(fz[v]);
                     out[v] = s;
                 }
-                store4<T, VECTOR>(py + t * a.D, out, cend - c);
+#pragma unroll
+                for (int v = 0; v < 4; v += 2) {
+                    f32x2 s = make_f32x2(out[v], out[v + 1]);
+                    if (a.D_skip) s = fma2(skip[v / 2], make_f32x2(fx[v], fx[v + 1]), s);
+                    if (pzo)
+                        s = mul2(s, mul2(make_f32x2(fz[v], fz[v + 1]),
+                                         make_f32x2(sigmoid_f32(fz[v]), sigmoid_f32(fz[v + 1]))));
+                    out[v] = lo_f32(s);
+                    out[v + 1] = hi_f32(s);
+                }
+                store4<T, VECTOR>(py + (size_t)(r * S::TPP) * a.D, out, full ? 4 : have);
             }
+            py += (size_t)kTile * a.D;
         };
 
         if (tiles) {
@@ -302,7 +360,10 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const ScanArgs a, int blo
         const T *pB = (const T *)a.Bm + b * a.bs.b + (size_t)g * N + n0;
         const T *pC = (const T *)a.Cm + b * a.cs.b + (size_t)g * N + n0;
         if (a.dt_bias) d += a.dt_bias[c];
-        if (a.softplus) d = softplus_f32(d);
+        if (a.softplus) {
+            f32x2 e;
+            d = lo_f32(softplus2(both(d), e));
+        }
         const float u = d * x, d2 = d * kLog2e;
         float4 r;
         r.x = fmaf(exp2_approx(d2 * A.x), h.x, u * to_f32<T>(pB[0]));

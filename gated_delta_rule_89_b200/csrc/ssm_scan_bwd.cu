@@ -181,8 +181,8 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const ulonglong2 du = *(const ulonglong2 *)(p[k] + (tb + t) * S::CB * 4);
-                        av[t][k][0] = exp2_approx2(mul2(du.x, A[k][0]));
-                        av[t][k][1] = exp2_approx2(mul2(du.x, A[k][1]));
+                        av[t][k][0] = decay2(du.x, A[k][0]);
+                        av[t][k][1] = decay2(du.x, A[k][1]);
                         hv[t + 1][k][0] = fma2(av[t][k][0], hv[t][k][0], mul2(du.y, bb.x));
                         hv[t + 1][k][1] = fma2(av[t][k][1], hv[t][k][1], mul2(du.y, bb.y));
                     }
@@ -298,7 +298,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     float d = fd[v] + bias[v];
-                    if (f.softplus) d = softplus_f32(d);
+                    if (f.softplus) { f32x2 e; d = lo_f32(softplus2(both(d), e)); }
                     if (!live || v >= have) d = 0.f;
                     const float u = d * fx[v];
                     dc[v] = pz ? fy[v] * (fz[v] * sigmoid_f32(fz[v])) : fy[v];
@@ -362,7 +362,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                             }
                         }
                         const float pre = fd[v] + bias[v];
-                        const float delta = f.softplus ? softplus_f32(pre) : pre;
+                        f32x2 e2; const float delta = f.softplus ? lo_f32(softplus2(both(pre), e2)) : pre;
                         float dc = fy[v];
                         if (pz) {
                             const float s = sigmoid_f32(fz[v]);
