@@ -150,26 +150,28 @@ __device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
 // fp32 rounding of its evaluation, 1.6e-7, is what is left).  A logarithm of
 // 1 + e would lose the digits of a small e in the sum; and time steps of 1e-3
 // have an e of 1e-3.  It also spares the special-function pipe one operation.
-__device__ __forceinline__ f32x2 log1p_unit2(f32x2 e)
+// (One value at a time: the coefficients are then immediate operands, while
+// the packed form wants each of them in a register pair.)
+__device__ __forceinline__ float log1p_unit(float e)
 {
-    f32x2 p = fma2(both(-0.0032440515f), e, both(0.01985158f));
-    p = fma2(p, e, both(-0.056959756f));
-    p = fma2(p, e, both(0.106036775f));
-    p = fma2(p, e, both(-0.15305606f));
-    p = fma2(p, e, both(0.19675943f));
-    p = fma2(p, e, both(-0.24954134f));
-    p = fma2(p, e, both(0.33329964f));
-    p = fma2(p, e, both(-0.49999902f));
-    p = fma2(p, e, both(1.f));
-    return mul2(p, e);
+    float p = -0.0032440515f;
+    p = fmaf(p, e, 0.01985158f);
+    p = fmaf(p, e, -0.056959756f);
+    p = fmaf(p, e, 0.106036775f);
+    p = fmaf(p, e, -0.15305606f);
+    p = fmaf(p, e, 0.19675943f);
+    p = fmaf(p, e, -0.24954134f);
+    p = fmaf(p, e, 0.33329964f);
+    p = fmaf(p, e, -0.49999902f);
+    p = fmaf(p, e, 1.f);
+    return p * e;
 }
-// log(1 + exp(x)) = max(x, 0) + log(1 + exp(-|x|)) of two values; a NaN stays
-// one.  `e` receives exp(-|x|).
-__device__ __forceinline__ f32x2 softplus2(f32x2 x, f32x2 &e)
+// log(1 + exp(x)) = max(x, 0) + log(1 + exp(-|x|)); a NaN stays one.  `e`
+// receives exp(-|x|).
+__device__ __forceinline__ float softplus_f32(float x, float &e)
 {
-    const float lo = lo_f32(x), hi = hi_f32(x);
-    e = make_f32x2(exp2_approx(-kLog2e * fabsf(lo)), exp2_approx(-kLog2e * fabsf(hi)));
-    return add2(make_f32x2(fmaxf(lo, 0.f), fmaxf(hi, 0.f)), log1p_unit2(e));
+    e = exp2_approx(-kLog2e * fabsf(x));
+    return fmaxf(x, 0.f) + log1p_unit(e);
 }
 
 // N consecutive elements from / to memory as fp32.  VECTOR: one access of
@@ -261,6 +263,21 @@ __device__ __forceinline__ void store4(T *p, const float *f, int valid)
             if (k < valid) p[k] = from_f32<T>(f[k]);
     }
 }
+
+// 4 states' B or C as they lie in shared memory, in the inputs' type, and in
+// two register pairs.  bf16 is widened by the lanes: 8 integer operations, but
+// half the shared-memory traffic, which otherwise bounds the scan.
+template <typename T> struct Quad;
+template <> struct Quad<float> {
+    ulonglong2 v;
+    __device__ __forceinline__ f32x2 lo() const { return v.x; }
+    __device__ __forceinline__ f32x2 hi() const { return v.y; }
+};
+template <> struct Quad<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ f32x2 lo() const { return make_f32x2(bf16_lo(v.x), bf16_hi(v.x)); }
+    __device__ __forceinline__ f32x2 hi() const { return make_f32x2(bf16_lo(v.y), bf16_hi(v.y)); }
+};
 
 inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 

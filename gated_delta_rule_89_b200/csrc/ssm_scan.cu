@@ -21,31 +21,36 @@ namespace gdr {
 namespace {
 
 constexpr int kSms = 148;
-constexpr int kScanLanes = 128;            // scan threads of a block: 4 states each
-constexpr int kScanThreads = 2 * kScanLanes;
+constexpr int kScanLanes = 128;            // threads of a block that run the recurrence
 constexpr int kTile = 32;                  // tokens between two block barriers
 
-// A block's share and its shared memory for state size N.
-template <int N> struct Shape {
+// A block's share and its shared memory, for state size N and CPT channels a
+// scan thread (4 states of each).  With two channels the B and C that a thread
+// loads serve twice, which matters: shared memory returns 128 bytes a clock,
+// and with one channel the loads of a token take 40 clocks of an SM against 32
+// for its exponentials.  With one channel there are twice as many blocks.
+template <typename T, int N, int CPT> struct Shape {
+    static constexpr int H = CPT == 1 && N > 16 ? kScanLanes : 2 * kScanLanes;   // helper threads
+    static constexpr int THREADS = kScanLanes + H;
     static constexpr int LPC = N / 4;                    // scan lanes of a channel
-    static constexpr int CB = kScanLanes / LPC;          // channels of a block
+    static constexpr int CB = kScanLanes / LPC * CPT;    // channels of a block
     static constexpr int GR = CB / 4;                    // groups of 4 channels
-    static constexpr int TPP = kScanLanes / GR;          // tokens the helpers cover at a time
+    static constexpr int TPP = H / GR;                   // tokens the helpers cover at a time
     static constexpr int R = TPP >= kTile ? 1 : kTile / TPP;
     static constexpr int GRB = N / 4;                    // groups of 4 states
-    static constexpr int TPB = kScanLanes / GRB;
+    static constexpr int TPB = H / GRB;
     static constexpr int RB = TPB >= kTile ? 1 : kTile / TPB;
-    static constexpr int P = kTile * CB * 4;             // floats: {delta, delta, u, u} per (token, channel)
-    static constexpr int S = kTile * N;                  // floats: B, and as many for C
-    static constexpr int Y = kTile * kScanLanes;         // floats: partial sums of C h
+    static constexpr int P = kTile * CB * 2;             // floats: {delta, u} per (token, channel)
+    static constexpr int S = kTile * N * sizeof(T) / 4;  // floats: B, and as many for C, in the inputs' type
+    static constexpr int Y = kTile * CB * LPC;           // floats: partial sums of C h
     static constexpr int BUF = P + 2 * S + Y;
     static constexpr size_t smem = 2 * BUF * sizeof(float);
 };
 
-// Shared-memory position of a 16-byte chunk: the helpers touch every 4th
-// (N = 16) chunk at a time, the scan lanes consecutive ones; with two bits of
-// the row of 8 folded in, both meet 8 different banks.
-__device__ __forceinline__ int swz(int chunk) { return chunk ^ ((chunk >> 3) & 3); }
+// Shared-memory position of a 16-byte chunk: the helpers touch every 2nd or
+// 4th chunk, the scan lanes consecutive ones; with the bits above a row of 8
+// folded in, both meet 8 different banks.
+__device__ __forceinline__ int swz(int chunk) { return chunk ^ ((chunk >> 3) & 7); }
 
 enum Mode {
     FULL,    // the outputs and the final state
@@ -63,11 +68,11 @@ struct Pieces {
     float *points;   // POINTS: [B][ceil(T / kCheckpoint)][D][N]
 };
 
-template <typename T, int N, bool VECTOR, Mode MODE>
-__global__ void __launch_bounds__(kScanThreads)
+template <typename T, int N, int CPT, bool VECTOR, Mode MODE>
+__global__ void __launch_bounds__(Shape<T, N, CPT>::THREADS)
 ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 {
-    using S = Shape<N>;
+    using S = Shape<T, N, CPT>;
     using V = typename Pack<T, 4>::V;
     extern __shared__ __align__(16) float sm[];
 
@@ -86,96 +91,125 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 
     if (tid < kScanLanes) {
         // -------------------------------------------------- the recurrence
-        const int ch = tid / S::LPC, n0 = (tid % S::LPC) * 4;
-        const int c = cfirst + ch;
-        const bool on = c < cend;
-        const size_t slot = (size_t)a.B * a.D * N, at = ((size_t)b * a.D + c) * N + n0;
-        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-        f32x2 A0 = 0, A1 = 0;
-        if (on) {
-            const float4 A = *(const float4 *)(a.A + (size_t)c * N + n0);
-            A0 = make_f32x2(A.x * kLog2e, A.y * kLog2e);
-            A1 = make_f32x2(A.z * kLog2e, A.w * kLog2e);
-            if (MODE == LOCAL) {
-                if (piece == 0) {
-                    // the second pass reads h0 from the slot, so that h_T may be the same buffer
-                    if (a.h0) h = *(const float4 *)(a.h0 + at);
-                    *(float4 *)(pc.slots + at) = h;
-                    h = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int ch = tid / S::LPC * CPT, ln = tid % S::LPC, n0 = ln * 4;
+        const size_t slot = (size_t)a.B * a.D * N, at = ((size_t)b * a.D + cfirst + ch) * N + n0;
+        bool on[CPT];
+        f32x2 A[CPT][2], h[CPT][2];
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            on[k] = cfirst + ch + k < cend;
+            const size_t ak = at + k * N;
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f), r = q;
+            if (on[k]) {
+                q = *(const float4 *)(a.A + (size_t)(cfirst + ch + k) * N + n0);
+                if (MODE == LOCAL) {
+                    if (piece == 0) {
+                        // the second pass reads h0 from the slot, so that h_T may be the same buffer
+                        if (a.h0) r = *(const float4 *)(a.h0 + ak);
+                        *(float4 *)(pc.slots + ak) = r;
+                        r = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                } else if (pc.count > 1) {
+                    r = *(const float4 *)(pc.slots + ak);
+                } else if (a.h0) {
+                    r = *(const float4 *)(a.h0 + ak);
                 }
-            } else if (pc.count > 1) {
-                h = *(const float4 *)(pc.slots + at);
-            } else if (a.h0) {
-                h = *(const float4 *)(a.h0 + at);
             }
+            A[k][0] = make_f32x2(q.x * kLog2e, q.y * kLog2e);
+            A[k][1] = make_f32x2(q.z * kLog2e, q.w * kLog2e);
+            h[k][0] = make_f32x2(r.x, r.y);
+            h[k][1] = make_f32x2(r.z, r.w);
+            if (MODE != LOCAL && on[k])
+                for (int s = 1; s <= piece; ++s) {   // fold in the pieces ahead
+                    const f32x2 sum = both(pc.sums[((size_t)s * a.B + b) * a.D + cfirst + ch + k]);
+                    const ulonglong2 v = *(const ulonglong2 *)(pc.slots + s * slot + ak);
+                    h[k][0] = fma2(decay2(sum, A[k][0]), h[k][0], v.x);
+                    h[k][1] = fma2(decay2(sum, A[k][1]), h[k][1], v.y);
+                }
         }
-        f32x2 h0 = make_f32x2(h.x, h.y), h1 = make_f32x2(h.z, h.w);
-        if (MODE != LOCAL && on)
-            for (int s = 1; s <= piece; ++s) {   // fold in the pieces ahead
-                const float sum = pc.sums[((size_t)s * a.B + b) * a.D + c];
-                const float4 q = *(const float4 *)(pc.slots + s * slot + at);
-                const f32x2 ss = make_f32x2(sum, sum);
-                h0 = fma2(decay2(ss, A0), h0, make_f32x2(q.x, q.y));
-                h1 = fma2(decay2(ss, A1), h1, make_f32x2(q.z, q.w));
-            }
-        float sum = 0.f;
+        float sum[CPT] = {};
         float *points = nullptr;
         if (MODE == POINTS)
-            points = pc.points + (((size_t)b * ((a.T + kCheckpoint - 1) / kCheckpoint) + t0 / kCheckpoint) * a.D + c) * N + n0;
+            points = pc.points +
+                     (((size_t)b * ((a.T + kCheckpoint - 1) / kCheckpoint) + t0 / kCheckpoint) * a.D + cfirst + ch) * N + n0;
         __syncthreads();
         // Four tokens' operands are loaded ahead of the four in work, and ahead of the stores of
         // their outputs: shared-memory loads are not moved across stores, and a warp that waited
         // for each token's loads would spend most of its time there.
         constexpr int G = 4;
         struct Token {
-            ulonglong2 du, b, c;
+            float du[2 * CPT];
+            Quad<T> b, c;
         };
         for (int i = 0; i < tiles; ++i) {
             const float *buf = sm + (i & 1) * S::BUF;
-            const float *p = buf + swz(ch) * 4, *sb = buf + S::P + n0, *sc = sb + S::S;
-            float *py = sm + (i & 1) * S::BUF + S::P + 2 * S::S + swz(tid >> 2) * 4 + (tid & 3);
+            const float *p = buf + swz(ch >> 1) * 4 + (ch & 1) * 2;
+            const T *sb = (const T *)(buf + S::P) + n0, *sc = (const T *)(buf + S::P + S::S) + n0;
+            float *py[CPT];
+#pragma unroll
+            for (int k = 0; k < CPT; ++k) {
+                const int s = (ch + k) * S::LPC + ln;
+                py[k] = sm + (i & 1) * S::BUF + S::P + 2 * S::S + swz(s >> 2) * 4 + (s & 3);
+            }
             Token now[G], next[G];
             auto fetch = [&](Token *k, int t) {
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    k[j].du = *(const ulonglong2 *)(p + (t + j) * S::CB * 4);
-                    k[j].b = *(const ulonglong2 *)(sb + (t + j) * N);
-                    if (MODE == FULL) k[j].c = *(const ulonglong2 *)(sc + (t + j) * N);
+                    const float *q = p + (t + j) * S::CB * 2;
+                    if (CPT == 2) *(float4 *)k[j].du = *(const float4 *)q;
+                    else *(float2 *)k[j].du = *(const float2 *)q;
+                    k[j].b = *(const Quad<T> *)(sb + (t + j) * N);
+                    if (MODE == FULL) k[j].c = *(const Quad<T> *)(sc + (t + j) * N);
                 }
             };
             fetch(now, 0);
 #pragma unroll
             for (int t = 0; t < kTile; t += G) {
-                if (MODE == POINTS && t % kCheckpoint == 0 && on && t0 + i * kTile + t < t1)
-                    *(ulonglong2 *)(points + (size_t)(i * kTile + t) / kCheckpoint * a.D * N) = make_ulonglong2(h0, h1);
+                if (MODE == POINTS && t % kCheckpoint == 0 && t0 + i * kTile + t < t1) {
+                    float *q = points + (size_t)(i * kTile + t) / kCheckpoint * a.D * N;
+#pragma unroll
+                    for (int k = 0; k < CPT; ++k)
+                        if (on[k]) *(ulonglong2 *)(q + k * N) = make_ulonglong2(h[k][0], h[k][1]);
+                }
                 if (t + G < kTile) fetch(next, t + G);
-                float y[G];
+                float y[G][CPT];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    const Token &k = now[j];
-                    h0 = fma2(decay2(k.du.x, A0), h0, mul2(k.du.y, k.b.x));
-                    h1 = fma2(decay2(k.du.x, A1), h1, mul2(k.du.y, k.b.y));
-                    if (MODE == FULL) {
-                        const f32x2 s = fma2(h1, k.c.y, mul2(h0, k.c.x));
-                        y[j] = lo_f32(s) + hi_f32(s);
-                    } else if (MODE == LOCAL) {
-                        sum += lo_f32(k.du.x);
+                    const Token &o = now[j];
+                    const f32x2 b0 = o.b.lo(), b1 = o.b.hi();
+#pragma unroll
+                    for (int k = 0; k < CPT; ++k) {
+                        const f32x2 d = both(o.du[2 * k]), u = both(o.du[2 * k + 1]);
+                        h[k][0] = fma2(decay2(d, A[k][0]), h[k][0], mul2(u, b0));
+                        h[k][1] = fma2(decay2(d, A[k][1]), h[k][1], mul2(u, b1));
+                        if (MODE == FULL) {
+                            const f32x2 s = fma2(h[k][1], o.c.hi(), mul2(h[k][0], o.c.lo()));
+                            y[j][k] = lo_f32(s) + hi_f32(s);
+                        } else if (MODE == LOCAL) {
+                            sum[k] += o.du[2 * k];
+                        }
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    if (MODE == FULL) py[(t + j) * kScanLanes] = y[j];
+                    if (MODE == FULL)
+#pragma unroll
+                        for (int k = 0; k < CPT; ++k) py[k][(t + j) * S::CB * S::LPC] = y[j][k];
                     now[j] = next[j];
                 }
             }
             __syncthreads();
         }
-        h = make_float4(lo_f32(h0), hi_f32(h0), lo_f32(h1), hi_f32(h1));
-        if (on && MODE == LOCAL) {
-            *(float4 *)(pc.slots + (piece + 1) * slot + at) = h;
-            if (n0 == 0) pc.sums[((size_t)(piece + 1) * a.B + b) * a.D + c] = sum;
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            if (!on[k]) continue;
+            const ulonglong2 v = make_ulonglong2(h[k][0], h[k][1]);
+            if (MODE == LOCAL) {
+                *(ulonglong2 *)(pc.slots + (piece + 1) * slot + at + k * N) = v;
+                if (ln == 0) pc.sums[((size_t)(piece + 1) * a.B + b) * a.D + cfirst + ch + k] = sum[k];
+            }
+            if (MODE == FULL && a.h_T && (t1 == len || pc.count == 1)) *(ulonglong2 *)(a.h_T + at + k * N) = v;
         }
-        if (on && MODE == FULL && a.h_T && (t1 == len || pc.count == 1)) *(float4 *)(a.h_T + at) = h;
     } else {
         // ------------- loads, time steps and outputs, one tile ahead and behind
         const int ht = tid - kScanLanes;
@@ -194,16 +228,11 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
         const T *pxo = px;                                     // and of the tile that is finished next
         const T *pzo = a.z ? (const T *)a.z + b * a.zs.b + c + first * a.zs.t : nullptr;
         T *py = (T *)a.y + ((size_t)b * a.T + first) * a.D + c;
-        f32x2 bias[2], skip[2];
-        {
-            float f[4], g[4];
+        float bias[4], skip[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                f[v] = a.dt_bias && v < have ? a.dt_bias[c + v] : 0.f;
-                g[v] = MODE == FULL && a.D_skip && v < have ? a.D_skip[c + v] : 0.f;
-            }
-            bias[0] = make_f32x2(f[0], f[1]), bias[1] = make_f32x2(f[2], f[3]);
-            skip[0] = make_f32x2(g[0], g[1]), skip[1] = make_f32x2(g[2], g[3]);
+        for (int v = 0; v < 4; ++v) {
+            bias[v] = a.dt_bias && v < have ? a.dt_bias[c + v] : 0.f;
+            skip[v] = MODE == FULL && a.D_skip && v < have ? a.D_skip[c + v] : 0.f;
         }
 
         V rx[S::R], rdt[S::R], rB[S::RB], rC[S::RB], ex[S::R], ez[S::R];
@@ -253,31 +282,24 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 float fx[4], fd[4];
                 unpack(rx[r], fx);
                 unpack(rdt[r], fd);
-                float *q = buf + k * S::CB * 4;
+                float *q = buf + k * S::CB * 2;
 #pragma unroll
-                for (int v = 0; v < 4; v += 2) {
-                    f32x2 e, d = add2(make_f32x2(fd[v], fd[v + 1]), bias[v / 2]);
-                    if (a.softplus) d = softplus2(d, e);
-                    if (!full) {                               // the state stands still
-                        const bool live = tb + k < t1;
-                        d = make_f32x2(live && v < have ? lo_f32(d) : 0.f, live && v + 1 < have ? hi_f32(d) : 0.f);
-                    }
-                    const f32x2 u = mul2(d, make_f32x2(fx[v], fx[v + 1]));
-                    *(float4 *)(q + swz(gr * 4 + v) * 4) = make_float4(lo_f32(d), lo_f32(d), lo_f32(u), lo_f32(u));
-                    *(float4 *)(q + swz(gr * 4 + v + 1) * 4) = make_float4(hi_f32(d), hi_f32(d), hi_f32(u), hi_f32(u));
+                for (int v = 0; v < 4; ++v) {
+                    float e, d = fd[v] + bias[v];
+                    if (a.softplus) d = softplus_f32(d, e);
+                    if (!full && (tb + k >= t1 || v >= have)) d = 0.f;   // the state stands still
+                    fd[v] = d;
+                    fx[v] *= d;
                 }
+                *(float4 *)(q + swz(gr * 2) * 4) = make_float4(fd[0], fx[0], fd[1], fx[1]);
+                *(float4 *)(q + swz(gr * 2 + 1) * 4) = make_float4(fd[2], fx[2], fd[3], fx[3]);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
                 if (S::TPB > kTile && k >= kTile) continue;
-                float f[4];
-                unpack(rB[r], f);
-                *(float4 *)(buf + S::P + k * N + grb * 4) = make_float4(f[0], f[1], f[2], f[3]);
-                if (MODE == FULL) {
-                    unpack(rC[r], f);
-                    *(float4 *)(buf + S::P + S::S + k * N + grb * 4) = make_float4(f[0], f[1], f[2], f[3]);
-                }
+                *(V *)((T *)(buf + S::P) + k * N + grb * 4) = rB[r];
+                if (MODE == FULL) *(V *)((T *)(buf + S::P + S::S) + k * N + grb * 4) = rC[r];
             }
         };
         auto finish = [&](int tile) {
@@ -292,7 +314,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 float part[N];                                  // the LPC partial sums of 4 channels
 #pragma unroll
                 for (int q = 0; q < N / 4; ++q)
-                    *(float4 *)(part + 4 * q) = *(const float4 *)(y + k * kScanLanes + swz(gr * (N / 4) + q) * 4);
+                    *(float4 *)(part + 4 * q) = *(const float4 *)(y + k * S::CB * S::LPC + swz(gr * (N / 4) + q) * 4);
                 float out[4], fx[4], fz[4];
                 unpack(ex[r], fx);
                 unpack(ez[r], fz);
@@ -301,17 +323,9 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                     float s = part[v * S::LPC];
 #pragma unroll
                     for (int l = 1; l < S::LPC; ++l) s += part[v * S::LPC + l];
+                    if (a.D_skip) s = fmaf(skip[v], fx[v], s);
+                    if (pzo) s *= fz[v] * sigmoid_f32(fz[v]);
                     out[v] = s;
-                }
-#pragma unroll
-                for (int v = 0; v < 4; v += 2) {
-                    f32x2 s = make_f32x2(out[v], out[v + 1]);
-                    if (a.D_skip) s = fma2(skip[v / 2], make_f32x2(fx[v], fx[v + 1]), s);
-                    if (pzo)
-                        s = mul2(s, mul2(make_f32x2(fz[v], fz[v + 1]),
-                                         make_f32x2(sigmoid_f32(fz[v]), sigmoid_f32(fz[v + 1]))));
-                    out[v] = lo_f32(s);
-                    out[v + 1] = hi_f32(s);
                 }
                 store4<T, VECTOR>(py + (size_t)(r * S::TPP) * a.D, out, full ? 4 : have);
             }
@@ -361,8 +375,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const ScanArgs a, int blo
         const T *pC = (const T *)a.Cm + b * a.cs.b + (size_t)g * N + n0;
         if (a.dt_bias) d += a.dt_bias[c];
         if (a.softplus) {
-            f32x2 e;
-            d = lo_f32(softplus2(both(d), e));
+            float e;
+            d = softplus_f32(d, e);
         }
         const float u = d * x, d2 = d * kLog2e;
         float4 r;
@@ -390,10 +404,26 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const ScanArgs a, int blo
 
 // --------------------------------------------------------------- launches
 
-int blocks_per_group(int D, int G, int N)
+int blocks_per_group(int D, int G, int N, int cpt)
 {
-    const int cb = 512 / N;
+    const int cb = 512 * cpt / N;
     return (D / G + cb - 1) / cb;
+}
+
+// One or two channels a thread, by how the blocks fill the SMs (two on each
+// either way).  Measured at N = 16 in us per 4096 tokens: one channel 264 for
+// a full set of 296 blocks and 204 for half of one, two channels 472 and 287;
+// so two are 11% faster where they fill the machine, and slower where half of
+// them would find no work (32-channel blocks against 64-channel ones: 2 x 4096
+// channels 527 and 574 us for 8192 tokens, 4 x 4096 channels 528 and 472 for 4096).
+int channels_per_thread(int B, int D, int G, int N)
+{
+    const long long set = 2 * kSms, groups = (long long)B * G;
+    auto cost = [&](int cpt, int full, int half) {
+        const long long blocks = groups * blocks_per_group(D, G, N, cpt), rest = blocks % set;
+        return blocks / set * full + (rest == 0 ? 0 : rest <= kSms ? half : full);
+    };
+    return cost(2, 472, 287) < cost(1, 264, 204) ? 2 : 1;
 }
 
 // Few channels leave most of the machine idle; then a row is cut into pieces
@@ -404,7 +434,7 @@ int blocks_per_group(int D, int G, int N)
 Pieces plan(int B, int T, int D, int G, int N, void *workspace)
 {
     Pieces p = {1, T, nullptr, nullptr, nullptr};
-    const long long blocks = (long long)B * G * blocks_per_group(D, G, N);
+    const long long blocks = (long long)B * G * blocks_per_group(D, G, N, channels_per_thread(B, D, G, N));
     if (blocks > 0 && blocks * 2 <= kSms && T >= 8 * kTile) {
         long long count = 2 * kSms / blocks;
         if (count > T / (4 * kTile)) count = T / (4 * kTile);
@@ -432,31 +462,42 @@ template <typename T> bool scan_vectors(const ScanArgs &a)
     return true;
 }
 
-template <typename T, int N, bool VECTOR, Mode MODE>
+template <typename T, int N, int CPT, bool VECTOR, Mode MODE>
 cudaError_t run_scan(const ScanArgs &a, const Pieces &p, int pieces, cudaStream_t st)
 {
-    auto k = ssm_scan_kernel<T, N, VECTOR, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<N>::smem);
+    using S = Shape<T, N, CPT>;
+    auto k = ssm_scan_kernel<T, N, CPT, VECTOR, MODE>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
     if (e != cudaSuccess) return e;
-    const int bpg = blocks_per_group(a.D, a.G, N);
-    k<<<dim3((unsigned)((long long)a.B * a.G * bpg), pieces), kScanThreads, Shape<N>::smem, st>>>(a, p, bpg);
+    const int bpg = blocks_per_group(a.D, a.G, N, CPT);
+    k<<<dim3((unsigned)((long long)a.B * a.G * bpg), pieces), S::THREADS, S::smem, st>>>(a, p, bpg);
     return cudaGetLastError();
 }
 
-template <typename T, int N, bool VECTOR>
+template <typename T, int N, int CPT, bool VECTOR>
 cudaError_t scan_typed(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
 {
     Pieces p = plan(a.B, a.T, a.D, a.G, N, a.workspace);
     cudaError_t e = cudaSuccess;
     if (p.count > 1) {
-        e = run_scan<T, N, VECTOR, LOCAL>(a, p, p.count - 1, st);
+        e = run_scan<T, N, CPT, VECTOR, LOCAL>(a, p, p.count - 1, st);
         if (e != cudaSuccess) return e;
         *launches += 1;
     }
     p.points = points;
-    e = points ? run_scan<T, N, VECTOR, POINTS>(a, p, p.count, st) : run_scan<T, N, VECTOR, FULL>(a, p, p.count, st);
+    e = points ? run_scan<T, N, CPT, VECTOR, POINTS>(a, p, p.count, st)
+               : run_scan<T, N, CPT, VECTOR, FULL>(a, p, p.count, st);
     if (e == cudaSuccess) *launches += 1;
     return e;
+}
+
+template <typename T, int N>
+cudaError_t scan_by_layout(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
+{
+    const bool v = scan_vectors<T>(a);
+    if (channels_per_thread(a.B, a.D, a.G, N) == 2)
+        return v ? scan_typed<T, N, 2, true>(a, points, st, launches) : scan_typed<T, N, 2, false>(a, points, st, launches);
+    return v ? scan_typed<T, N, 1, true>(a, points, st, launches) : scan_typed<T, N, 1, false>(a, points, st, launches);
 }
 
 template <typename T, int N>
@@ -470,11 +511,8 @@ cudaError_t step_typed(const ScanArgs &a, cudaStream_t st)
 template <int N>
 cudaError_t scan_n(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
 {
-    if (a.bf16)
-        return scan_vectors<__nv_bfloat16>(a) ? scan_typed<__nv_bfloat16, N, true>(a, points, st, launches)
-                                              : scan_typed<__nv_bfloat16, N, false>(a, points, st, launches);
-    return scan_vectors<float>(a) ? scan_typed<float, N, true>(a, points, st, launches)
-                                  : scan_typed<float, N, false>(a, points, st, launches);
+    return a.bf16 ? scan_by_layout<__nv_bfloat16, N>(a, points, st, launches)
+                  : scan_by_layout<float, N>(a, points, st, launches);
 }
 
 cudaError_t any_n(const ScanArgs &a, float *points, cudaStream_t st, int *launches)

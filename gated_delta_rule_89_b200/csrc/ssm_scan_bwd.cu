@@ -298,7 +298,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     float d = fd[v] + bias[v];
-                    if (f.softplus) { f32x2 e; d = lo_f32(softplus2(both(d), e)); }
+                    if (f.softplus) { float e; d = softplus_f32(d, e); }
                     if (!live || v >= have) d = 0.f;
                     const float u = d * fx[v];
                     dc[v] = pz ? fy[v] * (fz[v] * sigmoid_f32(fz[v])) : fy[v];
@@ -362,7 +362,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                             }
                         }
                         const float pre = fd[v] + bias[v];
-                        f32x2 e2; const float delta = f.softplus ? lo_f32(softplus2(both(pre), e2)) : pre;
+                        float e2; const float delta = f.softplus ? softplus_f32(pre, e2) : pre;
                         float dc = fy[v];
                         if (pz) {
                             const float s = sigmoid_f32(fz[v]);

@@ -56,6 +56,11 @@ CASES = [
     dict(B=1, T=700, D=40, N=16),                                    # pieces of a row
     dict(B=2, T=1100, D=8, N=8, G=2, dt=FP, lengths=[1100, 130]),
     dict(B=2, T=0, D=16, N=16),
+    # two channels a thread: as many blocks of twice the channels as fill two on most SMs
+    dict(B=230, T=37, D=36, N=16, lengths=[37, 0, 1, 33, 32] * 46),
+    dict(B=230, T=33, D=69, N=8, dt=FP),
+    dict(B=115, T=40, D=36, N=32, G=2, z=False),
+    dict(B=230, T=34, D=10, N=64, skip=False),
 ]
 
 
