@@ -71,6 +71,14 @@ size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N);
 constexpr int kCheckpoint = 8;
 cudaError_t launch_ssm_scan_checkpoints(const ScanArgs &a, float *states, cudaStream_t stream, int *launches);
 
+// For rows cut into `pieces` of `tokens` (a multiple of 32): what pieces 1 ..
+// pieces - 1 hand to the one ahead of them as the gradient of the state when
+// nothing comes from behind (slots[piece][B][D][N]) and their sums of delta
+// (sums[piece][B][D]).  `a` holds dy as x, Cm as Bm, and dt, A, z, dt_bias,
+// lengths of the forward.  Pieces behind a row's end are not written.
+cudaError_t launch_ssm_scan_adjoint(const ScanArgs &a, int pieces, int tokens, float *slots, float *sums,
+                                    cudaStream_t stream, int *launches);
+
 struct ScanBwdArgs {
     ScanArgs f;                                   // the forward's inputs (y, h_T unused)
     const void *dy;

@@ -55,7 +55,9 @@ __device__ __forceinline__ int swz(int chunk) { return chunk ^ ((chunk >> 3) & 7
 enum Mode {
     FULL,    // the outputs and the final state
     LOCAL,   // the state that a piece of a row ends with when it starts from zero
-    POINTS   // the states ahead of every kCheckpoint-th token, for the backward
+    POINTS,  // the states ahead of every kCheckpoint-th token, for the backward
+    ADJOINT  // the gradient of the state ahead of a piece when that behind it is zero: a walk back
+             // with dy silu(z) in the place of u and C in the place of B
 };
 
 // pieces of a row (time is split when there are few channels), tokens of a
@@ -67,6 +69,8 @@ struct Pieces {
     float *slots, *sums;
     float *points;   // POINTS: [B][ceil(T / kCheckpoint)][D][N]
 };
+// ADJOINT takes dy as x and Cm as Bm, and writes piece s's result to slots[s]
+// and its sum of delta to sums[s].
 
 template <typename T, int N, int CPT, bool VECTOR, Mode MODE>
 __global__ void __launch_bounds__(Shape<T, N, CPT>::THREADS)
@@ -82,7 +86,8 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
     const int cpg = a.D / a.G;
     const int cfirst = gi * cpg + (blockIdx.x - b * per_row - gi * blocks_per_group) * S::CB;
     const int cend = min(cfirst + S::CB, (gi + 1) * cpg);     // channels [cfirst, cend)
-    const int piece = blockIdx.y;
+    const int piece = blockIdx.y + (MODE == ADJOINT);         // nothing lies ahead of piece 0
+    constexpr bool kBack = MODE == ADJOINT;
     const int len = row_length(a.lengths, b, a.T);
     const int t0 = piece * pc.tokens, t1 = min(t0 + pc.tokens, len);
     if (piece > 0 && t0 >= t1) return;                        // the whole block
@@ -109,6 +114,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                         *(float4 *)(pc.slots + ak) = r;
                         r = make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+                } else if (MODE == ADJOINT) {
                 } else if (pc.count > 1) {
                     r = *(const float4 *)(pc.slots + ak);
                 } else if (a.h0) {
@@ -119,7 +125,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             A[k][1] = make_f32x2(q.z * kLog2e, q.w * kLog2e);
             h[k][0] = make_f32x2(r.x, r.y);
             h[k][1] = make_f32x2(r.z, r.w);
-            if (MODE != LOCAL && on[k])
+            if ((MODE == FULL || MODE == POINTS) && on[k])
                 for (int s = 1; s <= piece; ++s) {   // fold in the pieces ahead
                     const f32x2 sum = both(pc.sums[((size_t)s * a.B + b) * a.D + cfirst + ch + k]);
                     const ulonglong2 v = *(const ulonglong2 *)(pc.slots + s * slot + ak);
@@ -155,11 +161,12 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             auto fetch = [&](Token *k, int t) {
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    const float *q = p + (t + j) * S::CB * 2;
+                    const int at = kBack ? kTile - 1 - (t + j) : t + j;
+                    const float *q = p + at * S::CB * 2;
                     if (CPT == 2) *(float4 *)k[j].du = *(const float4 *)q;
                     else *(float2 *)k[j].du = *(const float2 *)q;
-                    k[j].b = *(const Quad<T> *)(sb + (t + j) * N);
-                    if (MODE == FULL) k[j].c = *(const Quad<T> *)(sc + (t + j) * N);
+                    k[j].b = *(const Quad<T> *)(sb + at * N);
+                    if (MODE == FULL) k[j].c = *(const Quad<T> *)(sc + at * N);
                 }
             };
             fetch(now, 0);
@@ -180,12 +187,17 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 #pragma unroll
                     for (int k = 0; k < CPT; ++k) {
                         const f32x2 d = both(o.du[2 * k]), u = both(o.du[2 * k + 1]);
-                        h[k][0] = fma2(decay2(d, A[k][0]), h[k][0], mul2(u, b0));
-                        h[k][1] = fma2(decay2(d, A[k][1]), h[k][1], mul2(u, b1));
+                        if (kBack) {   // u is dy silu(z), b is C
+                            h[k][0] = mul2(decay2(d, A[k][0]), fma2(u, b0, h[k][0]));
+                            h[k][1] = mul2(decay2(d, A[k][1]), fma2(u, b1, h[k][1]));
+                        } else {
+                            h[k][0] = fma2(decay2(d, A[k][0]), h[k][0], mul2(u, b0));
+                            h[k][1] = fma2(decay2(d, A[k][1]), h[k][1], mul2(u, b1));
+                        }
                         if (MODE == FULL) {
                             const f32x2 s = fma2(h[k][1], o.c.hi(), mul2(h[k][0], o.c.lo()));
                             y[j][k] = lo_f32(s) + hi_f32(s);
-                        } else if (MODE == LOCAL) {
+                        } else if (MODE != POINTS) {
                             sum[k] += o.du[2 * k];
                         }
                     }
@@ -204,9 +216,10 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
         for (int k = 0; k < CPT; ++k) {
             if (!on[k]) continue;
             const ulonglong2 v = make_ulonglong2(h[k][0], h[k][1]);
-            if (MODE == LOCAL) {
-                *(ulonglong2 *)(pc.slots + (piece + 1) * slot + at + k * N) = v;
-                if (ln == 0) pc.sums[((size_t)(piece + 1) * a.B + b) * a.D + cfirst + ch + k] = sum[k];
+            if (MODE == LOCAL || MODE == ADJOINT) {
+                const int s = kBack ? piece : piece + 1;
+                *(ulonglong2 *)(pc.slots + s * slot + at + k * N) = v;
+                if (ln == 0) pc.sums[((size_t)s * a.B + b) * a.D + cfirst + ch + k] = sum[k];
             }
             if (MODE == FULL && a.h_T && (t1 == len || pc.count == 1)) *(ulonglong2 *)(a.h_T + at + k * N) = v;
         }
@@ -220,7 +233,10 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
         // every group of 4 whole: the tiles that lie inside the piece take no bounds checks
         const bool whole = cfirst + S::CB <= cend;
         // running pointers to this thread's first element of the tile that is fetched next
-        const long long first = (long long)t0 + tok, firstb = (long long)t0 + tokb;
+        constexpr int kStep = kBack ? -kTile : kTile;
+        const long long begin = (long long)t0 + (kBack && tiles ? (long long)(tiles - 1) * kTile : 0);
+        const long long first = begin + tok, firstb = begin + tokb;
+        auto token_of = [&](int i) { return t0 + (kBack ? tiles - 1 - i : i) * kTile; };   // of the i-th tile
         const T *px = (const T *)a.x + b * a.xs.b + c + first * a.xs.t;
         const T *pdt = (const T *)a.dt + b * a.dts.b + c + first * a.dts.t;
         const T *pB = (const T *)a.Bm + b * a.bs.b + (size_t)gi * N + grb * 4 + firstb * a.bs.t;
@@ -235,9 +251,10 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             skip[v] = MODE == FULL && a.D_skip && v < have ? a.D_skip[c + v] : 0.f;
         }
 
-        V rx[S::R], rdt[S::R], rB[S::RB], rC[S::RB], ex[S::R], ez[S::R];
-        auto fetch = [&](int tile) {
-            const int tb = t0 + tile * kTile;
+        V rx[S::R], rdt[S::R], rB[S::RB], rC[S::RB], ex[S::R], ez[S::R], rz[S::R];
+        const T *pz = kBack ? pzo : nullptr;
+        auto fetch = [&](int i) {
+            const int tb = token_of(i);
             const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
@@ -245,6 +262,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
                 rx[r] = load4<T, VECTOR>(px + r * S::TPP * a.xs.t, valid);
                 rdt[r] = load4<T, VECTOR>(pdt + r * S::TPP * a.dts.t, valid);
+                if (kBack && pz) rz[r] = load4<T, VECTOR>(pz + r * S::TPP * a.zs.t, valid);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
@@ -253,10 +271,11 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 rB[r] = load4<T, VECTOR>(pB + r * S::TPB * a.bs.t, valid);
                 if (MODE == FULL) rC[r] = load4<T, VECTOR>(pC + r * S::TPB * a.cs.t, valid);
             }
-            px += kTile * a.xs.t;
-            pdt += kTile * a.dts.t;
-            pB += kTile * a.bs.t;
-            pC += kTile * a.cs.t;
+            px += kStep * a.xs.t;
+            pdt += kStep * a.dts.t;
+            pB += kStep * a.bs.t;
+            if (MODE == FULL) pC += kStep * a.cs.t;
+            if (kBack && pz) pz += kStep * a.zs.t;
         };
         auto fetch_out = [&](int tile) {
             const int tb = t0 + tile * kTile;
@@ -271,17 +290,18 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             pxo += kTile * a.xs.t;
             if (pzo) pzo += kTile * a.zs.t;
         };
-        auto prepare = [&](int tile) {
-            float *buf = sm + (tile & 1) * S::BUF;
-            const int tb = t0 + tile * kTile;
+        auto prepare = [&](int i) {
+            float *buf = sm + (i & 1) * S::BUF;
+            const int tb = token_of(i);
             const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
                 if (S::TPP > kTile && k >= kTile) continue;
-                float fx[4], fd[4];
+                float fx[4], fd[4], fz[4];
                 unpack(rx[r], fx);
                 unpack(rdt[r], fd);
+                if (kBack && pz) unpack(rz[r], fz);
                 float *q = buf + k * S::CB * 2;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
@@ -289,7 +309,8 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                     if (a.softplus) d = softplus_f32(d, e);
                     if (!full && (tb + k >= t1 || v >= have)) d = 0.f;   // the state stands still
                     fd[v] = d;
-                    fx[v] *= d;
+                    if (!kBack) fx[v] *= d;
+                    else if (pz) fx[v] *= fz[v] * sigmoid_f32(fz[v]);
                 }
                 *(float4 *)(q + swz(gr * 2) * 4) = make_float4(fd[0], fx[0], fd[1], fx[1]);
                 *(float4 *)(q + swz(gr * 2 + 1) * 4) = make_float4(fd[2], fx[2], fd[3], fx[3]);
@@ -474,30 +495,43 @@ cudaError_t run_scan(const ScanArgs &a, const Pieces &p, int pieces, cudaStream_
     return cudaGetLastError();
 }
 
+// What a call wants besides the outputs: the states for the backward, or only
+// the backward's walk over its pieces.
+struct Extra {
+    float *points = nullptr;
+    bool adjoint = false;
+    Pieces back = {};
+};
+
 template <typename T, int N, int CPT, bool VECTOR>
-cudaError_t scan_typed(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
+cudaError_t scan_typed(const ScanArgs &a, const Extra &x, cudaStream_t st, int *launches)
 {
-    Pieces p = plan(a.B, a.T, a.D, a.G, N, a.workspace);
     cudaError_t e = cudaSuccess;
+    if (x.adjoint) {
+        e = run_scan<T, N, CPT, VECTOR, ADJOINT>(a, x.back, x.back.count - 1, st);
+        if (e == cudaSuccess) *launches += 1;
+        return e;
+    }
+    Pieces p = plan(a.B, a.T, a.D, a.G, N, a.workspace);
     if (p.count > 1) {
         e = run_scan<T, N, CPT, VECTOR, LOCAL>(a, p, p.count - 1, st);
         if (e != cudaSuccess) return e;
         *launches += 1;
     }
-    p.points = points;
-    e = points ? run_scan<T, N, CPT, VECTOR, POINTS>(a, p, p.count, st)
+    p.points = x.points;
+    e = x.points ? run_scan<T, N, CPT, VECTOR, POINTS>(a, p, p.count, st)
                : run_scan<T, N, CPT, VECTOR, FULL>(a, p, p.count, st);
     if (e == cudaSuccess) *launches += 1;
     return e;
 }
 
 template <typename T, int N>
-cudaError_t scan_by_layout(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
+cudaError_t scan_by_layout(const ScanArgs &a, const Extra &x, cudaStream_t st, int *launches)
 {
     const bool v = scan_vectors<T>(a);
     if (channels_per_thread(a.B, a.D, a.G, N) == 2)
-        return v ? scan_typed<T, N, 2, true>(a, points, st, launches) : scan_typed<T, N, 2, false>(a, points, st, launches);
-    return v ? scan_typed<T, N, 1, true>(a, points, st, launches) : scan_typed<T, N, 1, false>(a, points, st, launches);
+        return v ? scan_typed<T, N, 2, true>(a, x, st, launches) : scan_typed<T, N, 2, false>(a, x, st, launches);
+    return v ? scan_typed<T, N, 1, true>(a, x, st, launches) : scan_typed<T, N, 1, false>(a, x, st, launches);
 }
 
 template <typename T, int N>
@@ -509,19 +543,19 @@ cudaError_t step_typed(const ScanArgs &a, cudaStream_t st)
 }
 
 template <int N>
-cudaError_t scan_n(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
+cudaError_t scan_n(const ScanArgs &a, const Extra &x, cudaStream_t st, int *launches)
 {
-    return a.bf16 ? scan_by_layout<__nv_bfloat16, N>(a, points, st, launches)
-                  : scan_by_layout<float, N>(a, points, st, launches);
+    return a.bf16 ? scan_by_layout<__nv_bfloat16, N>(a, x, st, launches)
+                  : scan_by_layout<float, N>(a, x, st, launches);
 }
 
-cudaError_t any_n(const ScanArgs &a, float *points, cudaStream_t st, int *launches)
+cudaError_t any_n(const ScanArgs &a, const Extra &x, cudaStream_t st, int *launches)
 {
     switch (a.N) {
-        case 8: return scan_n<8>(a, points, st, launches);
-        case 16: return scan_n<16>(a, points, st, launches);
-        case 32: return scan_n<32>(a, points, st, launches);
-        default: return scan_n<64>(a, points, st, launches);
+        case 8: return scan_n<8>(a, x, st, launches);
+        case 16: return scan_n<16>(a, x, st, launches);
+        case 32: return scan_n<32>(a, x, st, launches);
+        default: return scan_n<64>(a, x, st, launches);
     }
 }
 
@@ -535,12 +569,23 @@ size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int G, int N)
 
 cudaError_t launch_ssm_scan_fwd(const ScanArgs &a, cudaStream_t stream, int *launches)
 {
-    return any_n(a, nullptr, stream, launches);
+    return any_n(a, Extra{}, stream, launches);
 }
 
 cudaError_t launch_ssm_scan_checkpoints(const ScanArgs &a, float *states, cudaStream_t stream, int *launches)
 {
-    return any_n(a, states, stream, launches);
+    Extra x;
+    x.points = states;
+    return any_n(a, x, stream, launches);
+}
+
+cudaError_t launch_ssm_scan_adjoint(const ScanArgs &a, int pieces, int tokens, float *slots, float *sums,
+                                    cudaStream_t stream, int *launches)
+{
+    Extra x;
+    x.adjoint = true;
+    x.back = {pieces, tokens, slots, sums, nullptr};
+    return any_n(a, x, stream, launches);
 }
 
 cudaError_t launch_ssm_scan_step(const ScanArgs &a, cudaStream_t stream, int *launches)

@@ -28,31 +28,44 @@
 namespace gdr {
 namespace {
 
+constexpr int kSms = 148;
 constexpr int kLanes = 128;              // threads that walk: 4 states x 2 channels each
-constexpr int kThreads = 2 * kLanes;     // and as many helpers
+constexpr int kHelpers = 256;            // threads that load, form the time steps and write the results
+constexpr int kThreads = kLanes + kHelpers;
 constexpr int kTile = 16;                // tokens between two block barriers
 constexpr int kSub = kCheckpoint;        // tokens recomputed at a time
+// Registers a thread: the launch gives every thread 168; the walk keeps 8
+// tokens' decays and states and takes 240, which the helpers make room for
+// (128 * 240 + 256 * 128 = 63488 <= 384 * 168 = 64512).
+constexpr int kWalkRegs = 240, kHelperRegs = 128;
 
-template <int N> struct Shape {
+template <typename T, int N> struct Shape {
     static constexpr int LN = N / 4;                   // lanes of a channel
-    static constexpr int CL = 32 / LN;                 // channels side by side in a warp
+    static constexpr int CL = 32 / LN;                 // pairs of channels side by side in a warp
     static constexpr int CW = 2 * CL;                  // channels of a warp
     static constexpr int CB = 4 * CW;                  // channels of a block
     static constexpr int GR = CB / 4;
-    static constexpr int TPP = kLanes / GR;
+    static constexpr int TPP = kHelpers / GR;
     static constexpr int R = TPP >= kTile ? 1 : kTile / TPP;
     static constexpr int GRB = N / 4;
-    static constexpr int TPB = kLanes / GRB;
+    static constexpr int TPB = kHelpers / GRB;
     static constexpr int RB = TPB >= kTile ? 1 : kTile / TPB;
     // floats of one buffer
-    static constexpr int P = kTile * CB * 4;           // {delta, delta, u, u}
-    static constexpr int DC = kTile * CB * 2;          // {dc, dc}
-    static constexpr int S = kTile * N;                // B, then C
+    static constexpr int P = kTile * CB * 2;           // {delta, u}
+    static constexpr int DC = kTile * CB;              // dc
+    static constexpr int S = kTile * N * sizeof(T) / 4;   // B, then C, in the inputs' type
     static constexpr int Y2 = kTile * 2 * kLanes * 2;  // {du, sum w A2} of each lane and channel
     static constexpr int Y1 = kTile * 2 * kLanes;      // C h of each lane and channel
     static constexpr int Q = kTile * 4 * 2 * N;        // the warps' sums of dB and dC
     static constexpr int BUF = P + DC + 2 * S + Y2 + Y1 + Q;
     static constexpr size_t smem = 2 * BUF * sizeof(float);
+};
+
+// Pieces that a row is walked in (side by side, when there are few channels),
+// tokens of a piece, and what the pieces behind hand on: launch_ssm_scan_adjoint.
+struct BackPieces {
+    int count, tokens;
+    float *slots, *sums;
 };
 
 // Shared-memory position of a 16-byte chunk.  The helpers touch chunks 2, 4 or
@@ -63,8 +76,9 @@ __device__ __forceinline__ int swz(int chunk) { return chunk ^ ((chunk >> 3) & 7
 struct BwdParts {
     float *points;     // states ahead of every kSub-th token
     float *bc;         // [blocks of a group][B][T][G][2][N]: parts of dB and dC
-    float *dA;         // [B][D][N]
-    float *dD, *dbias; // [B][D]
+    float *dA;         // [pieces * B][D][N]
+    float *dD, *dbias; // [pieces * B][D]
+    BackPieces pc;
 };
 
 // Sums v[0..COUNT) over the lanes that differ in the bits from MASK up to 16.
@@ -96,10 +110,11 @@ template <typename T, int N, bool VECTOR>
 __global__ void __launch_bounds__(kThreads, 1)
 ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
 {
-    using S = Shape<N>;
+    using S = Shape<T, N>;
     using V = typename Pack<T, 4>::V;
     extern __shared__ __align__(16) float sm[];
     const ScanArgs &f = a.f;
+    const BackPieces &pc = parts.pc;
 
     const int per_row = blocks_per_group * f.G;
     const int b = blockIdx.x / per_row;
@@ -109,122 +124,153 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
     const int cfirst = gi * cpg + blk * S::CB;
     const int cend = min(cfirst + S::CB, (gi + 1) * cpg);
     const int len = row_length(f.lengths, b, f.T);
-    const int tiles = (len + kTile - 1) / kTile;
+    const int piece = blockIdx.y, t0 = piece * pc.tokens;     // a multiple of kTile
+    const int stop = min(t0 + pc.tokens, f.T);                // rows [t0, stop) are this piece's
+    const int t1 = min(stop, len);
+    const int tiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;
     const int tid = threadIdx.x;
+    const size_t row_of_parts = (size_t)piece * f.B + b;
 
     if (tid < kLanes) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWalkRegs));
         const int warp = tid >> 5, lane = tid & 31;
         const int ln = lane % S::LN, n0 = ln * 4;
-        int ch[2];
+        const int ch = warp * S::CW + lane / S::LN * 2;       // and ch + 1
+        const size_t at = ((size_t)b * f.D + cfirst + ch) * N + n0;
         bool on[2];
-        size_t at[2];
         f32x2 A[2][2], carry[2][2], dA[2][2];
-        const float *point[2];
-        const size_t pstride = (size_t)f.D * N;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            ch[k] = warp * S::CW + k * S::CL + lane / S::LN;
-            const int c = cfirst + ch[k];
-            on[k] = c < cend;
-            at[k] = ((size_t)b * f.D + c) * N + n0;
+            on[k] = cfirst + ch + k < cend;
             float4 q = make_float4(0.f, 0.f, 0.f, 0.f), r = q;
             if (on[k]) {
-                q = *(const float4 *)(f.A + (size_t)c * N + n0);
-                if (a.dh_T) r = *(const float4 *)(a.dh_T + at[k]);
+                q = *(const float4 *)(f.A + (size_t)(cfirst + ch + k) * N + n0);
+                if (a.dh_T) r = *(const float4 *)(a.dh_T + at + k * N);
             }
             A[k][0] = make_f32x2(q.x * kLog2e, q.y * kLog2e);
             A[k][1] = make_f32x2(q.z * kLog2e, q.w * kLog2e);
             carry[k][0] = make_f32x2(r.x, r.y);
             carry[k][1] = make_f32x2(r.z, r.w);
             dA[k][0] = dA[k][1] = 0;
-            point[k] = parts.points + ((size_t)b * ((f.T + kSub - 1) / kSub) * f.D + c) * N + n0;
+            // fold in the pieces behind, the last that the row has first
+            if (pc.count > 1 && on[k])
+                for (int s = (len - 1) / pc.tokens; s > piece; --s) {
+                    const f32x2 sum = both(pc.sums[((size_t)s * f.B + b) * f.D + cfirst + ch + k]);
+                    const ulonglong2 v = *(const ulonglong2 *)(pc.slots + (size_t)s * f.B * f.D * N + at + k * N);
+                    carry[k][0] = fma2(decay2(sum, A[k][0]), carry[k][0], v.x);
+                    carry[k][1] = fma2(decay2(sum, A[k][1]), carry[k][1], v.y);
+                }
         }
-        // the stored state ahead of the sub-tile that comes next
-        ulonglong2 next[2] = {make_ulonglong2(0, 0), make_ulonglong2(0, 0)};
-        auto fetch_state = [&](int sub) {
+        // the stored states ahead of the sub-tile that comes next
+        const size_t pstride = (size_t)f.D * N;
+        const float *point = parts.points + ((size_t)b * ((f.T + kSub - 1) / kSub) * f.D + cfirst + ch) * N + n0;
+        ulonglong2 state[2] = {make_ulonglong2(0, 0), make_ulonglong2(0, 0)};
+        auto fetch_state = [&](int t) {
+            if (t >= t0 && t < t1)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (on[k] && sub >= 0 && sub * kSub < len)
-                    next[k] = *(const ulonglong2 *)(point[k] + (size_t)sub * pstride);
+                for (int k = 0; k < 2; ++k)
+                    if (on[k]) state[k] = *(const ulonglong2 *)(point + (size_t)(t / kSub) * pstride + k * N);
         };
-        fetch_state((tiles - 1) * (kTile / kSub) + kTile / kSub - 1);
+        fetch_state(t0 + tiles * kTile - kSub);
         __syncthreads();
         for (int i = 0; i < tiles; ++i) {
-            const int tile = tiles - 1 - i;
+            const int tb0 = t0 + (tiles - 1 - i) * kTile;
             float *buf = sm + (i & 1) * S::BUF;
-            const float *sB = buf + S::P + S::DC + n0, *sC = sB + S::S;
-            float *y2 = buf + S::P + S::DC + 2 * S::S, *y1 = y2 + S::Y2, *sq = y1 + S::Y1;
-            const float *p[2], *pd[2];
+            const float *p = buf + swz(ch >> 1) * 4, *pd = buf + S::P + swz(ch >> 2) * 4 + (ch & 2);
+            const T *sB = (const T *)(buf + S::P + S::DC) + n0, *sC = (const T *)(buf + S::P + S::DC + S::S) + n0;
+            float *y2 = buf + S::P + S::DC + 2 * S::S, *y1 = y2 + S::Y2;
+            float *sq = y1 + S::Y1 + warp * 2 * N + n0;
             float *o2[2], *o1[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                p[k] = buf + swz(ch[k]) * 4;
-                pd[k] = buf + S::P + swz(ch[k] >> 1) * 4 + (ch[k] & 1) * 2;
-                const int s = ch[k] * S::LN + ln;
+                const int s = (ch + k) * S::LN + ln;
                 o2[k] = y2 + swz(s >> 1) * 4 + (s & 1) * 2;
                 o1[k] = y1 + swz(s >> 2) * 4 + (s & 3);
             }
+#pragma unroll 1
             for (int sub = kTile / kSub - 1; sub >= 0; --sub) {
                 const int tb = sub * kSub;
                 f32x2 av[kSub][2][2], hv[kSub + 1][2][2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    hv[0][k][0] = next[k].x;
-                    hv[0][k][1] = next[k].y;
+                    hv[0][k][0] = state[k].x;
+                    hv[0][k][1] = state[k].y;
                 }
-                // a sub-tile behind the row's end has no stored state; its tokens change nothing and
-                // what is computed for them is not written, but the state must be finite
-                fetch_state(tile * (kTile / kSub) + sub - 1);
+                // A sub-tile behind the row's end has no stored state (it is 0 then); its tokens
+                // have delta = dc = 0 and change nothing.
+                fetch_state(tb0 + tb - kSub);
 #pragma unroll
                 for (int t = 0; t < kSub; ++t) {
-                    const ulonglong2 bb = *(const ulonglong2 *)(sB + (tb + t) * N);
+                    const float4 du = *(const float4 *)(p + (tb + t) * S::CB * 2);
+                    const Quad<T> bq = *(const Quad<T> *)(sB + (tb + t) * N);
+                    const f32x2 b0 = bq.lo(), b1 = bq.hi();
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const ulonglong2 du = *(const ulonglong2 *)(p[k] + (tb + t) * S::CB * 4);
-                        av[t][k][0] = decay2(du.x, A[k][0]);
-                        av[t][k][1] = decay2(du.x, A[k][1]);
-                        hv[t + 1][k][0] = fma2(av[t][k][0], hv[t][k][0], mul2(du.y, bb.x));
-                        hv[t + 1][k][1] = fma2(av[t][k][1], hv[t][k][1], mul2(du.y, bb.y));
+                        const f32x2 d = both(k ? du.z : du.x), u = both(k ? du.w : du.y);
+                        av[t][k][0] = decay2(d, A[k][0]);
+                        av[t][k][1] = decay2(d, A[k][1]);
+                        hv[t + 1][k][0] = fma2(av[t][k][0], hv[t][k][0], mul2(u, b0));
+                        hv[t + 1][k][1] = fma2(av[t][k][1], hv[t][k][1], mul2(u, b1));
                     }
                 }
+                // A token's operands are loaded ahead of the stores of the token before it.
+                struct Token {
+                    float4 du;
+                    float2 dc;
+                    Quad<T> b, c;
+                } now, next;
+                auto fetch = [&](Token &k, int t) {
+                    k.du = *(const float4 *)(p + t * S::CB * 2);
+                    k.dc = *(const float2 *)(pd + t * S::CB);
+                    k.b = *(const Quad<T> *)(sB + t * N);
+                    k.c = *(const Quad<T> *)(sC + t * N);
+                };
+                fetch(now, tb + kSub - 1);
 #pragma unroll
                 for (int t = kSub - 1; t >= 0; --t) {
-                    const ulonglong2 bb = *(const ulonglong2 *)(sB + (tb + t) * N);
-                    const ulonglong2 cc = *(const ulonglong2 *)(sC + (tb + t) * N);
-                    f32x2 dB[2], dC[2];
+                    if (t > 0) fetch(next, tb + t - 1);
+                    const f32x2 b0 = now.b.lo(), b1 = now.b.hi(), c0 = now.c.lo(), c1 = now.c.hi();
+                    f32x2 dB0, dB1, dC0, dC1;
+                    float su[2], sw[2], sy[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const ulonglong2 du = *(const ulonglong2 *)(p[k] + (tb + t) * S::CB * 4);
-                        const f32x2 dc = *(const f32x2 *)(pd[k] + (tb + t) * S::CB * 2);
-                        const f32x2 g0 = fma2(dc, cc.x, carry[k][0]), g1 = fma2(dc, cc.y, carry[k][1]);
-                        dB[0] = k ? fma2(g0, du.y, dB[0]) : mul2(g0, du.y);
-                        dB[1] = k ? fma2(g1, du.y, dB[1]) : mul2(g1, du.y);
-                        dC[0] = k ? fma2(dc, hv[t + 1][k][0], dC[0]) : mul2(dc, hv[t + 1][k][0]);
-                        dC[1] = k ? fma2(dc, hv[t + 1][k][1], dC[1]) : mul2(dc, hv[t + 1][k][1]);
-                        const f32x2 su = fma2(g1, bb.y, mul2(g0, bb.x));
+                        const f32x2 d = both(k ? now.du.z : now.du.x), u = both(k ? now.du.w : now.du.y);
+                        const f32x2 dc = both(k ? now.dc.y : now.dc.x);
+                        const f32x2 g0 = fma2(dc, c0, carry[k][0]), g1 = fma2(dc, c1, carry[k][1]);
+                        dB0 = k ? fma2(g0, u, dB0) : mul2(g0, u);
+                        dB1 = k ? fma2(g1, u, dB1) : mul2(g1, u);
+                        dC0 = k ? fma2(dc, hv[t + 1][k][0], dC0) : mul2(dc, hv[t + 1][k][0]);
+                        dC1 = k ? fma2(dc, hv[t + 1][k][1], dC1) : mul2(dc, hv[t + 1][k][1]);
+                        const f32x2 pu = fma2(g1, b1, mul2(g0, b0));
                         carry[k][0] = mul2(av[t][k][0], g0);
                         carry[k][1] = mul2(av[t][k][1], g1);
                         const f32x2 w0 = mul2(carry[k][0], hv[t][k][0]), w1 = mul2(carry[k][1], hv[t][k][1]);
-                        const f32x2 sw = fma2(w1, A[k][1], mul2(w0, A[k][0]));
-                        dA[k][0] = fma2(w0, du.x, dA[k][0]);
-                        dA[k][1] = fma2(w1, du.x, dA[k][1]);
-                        *(float2 *)(o2[k] + (tb + t) * kLanes * 4) =
-                            make_float2(lo_f32(su) + hi_f32(su), lo_f32(sw) + hi_f32(sw));
+                        const f32x2 pw = fma2(w1, A[k][1], mul2(w0, A[k][0]));
+                        dA[k][0] = fma2(w0, d, dA[k][0]);
+                        dA[k][1] = fma2(w1, d, dA[k][1]);
+                        su[k] = lo_f32(pu) + hi_f32(pu);
+                        sw[k] = lo_f32(pw) + hi_f32(pw);
                         if (f.z) {
-                            const f32x2 y = fma2(hv[t + 1][k][1], cc.y, mul2(hv[t + 1][k][0], cc.x));
-                            o1[k][(tb + t) * kLanes * 2] = lo_f32(y) + hi_f32(y);
+                            const f32x2 y = fma2(hv[t + 1][k][1], c1, mul2(hv[t + 1][k][0], c0));
+                            sy[k] = lo_f32(y) + hi_f32(y);
                         }
                     }
-                    float v[8] = {lo_f32(dB[0]), hi_f32(dB[0]), lo_f32(dB[1]), hi_f32(dB[1]),
-                                  lo_f32(dC[0]), hi_f32(dC[0]), lo_f32(dC[1]), hi_f32(dC[1])};
+                    float v[8] = {lo_f32(dB0), hi_f32(dB0), lo_f32(dB1), hi_f32(dB1),
+                                  lo_f32(dC0), hi_f32(dC0), lo_f32(dC1), hi_f32(dC1)};
                     int which = 0;
                     lane_sums<8, S::LN>(v, lane, which);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        *(float2 *)(o2[k] + (tb + t) * kLanes * 4) = make_float2(su[k], sw[k]);
+                        if (f.z) o1[k][(tb + t) * kLanes * 2] = sy[k];
+                    }
                     constexpr int left = 8 / S::CL > 1 ? 8 / S::CL : 1;
                     if (S::CL <= 8 || lane < 16) {
-                        float *o = sq + ((tb + t) * 4 + warp) * 2 * N + (which >> 2) * N + n0 + (which & 3);
+                        float *o = sq + (tb + t) * 8 * N + (which >> 2) * N + (which & 3);
 #pragma unroll
                         for (int j = 0; j < left; ++j) o[j] = v[j];
                     }
+                    now = next;
                 }
             }
             __syncthreads();
@@ -232,221 +278,229 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (on[k]) {
-                *(float4 *)(parts.dA + at[k]) =
-                    make_float4(lo_f32(dA[k][0]), hi_f32(dA[k][0]), lo_f32(dA[k][1]), hi_f32(dA[k][1]));
-                if (a.dh0)
-                    *(float4 *)(a.dh0 + at[k]) = make_float4(lo_f32(carry[k][0]), hi_f32(carry[k][0]),
-                                                             lo_f32(carry[k][1]), hi_f32(carry[k][1]));
+                *(ulonglong2 *)(parts.dA + row_of_parts * f.D * N + (size_t)(cfirst + ch + k) * N + n0) =
+                    make_ulonglong2(dA[k][0], dA[k][1]);
+                if (a.dh0 && piece == 0) *(ulonglong2 *)(a.dh0 + at + k * N) = make_ulonglong2(carry[k][0], carry[k][1]);
             }
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHelperRegs));
         const int ht = tid - kLanes;
         const int gr = ht % S::GR, tok = ht / S::GR;
         const int grb = ht % S::GRB, tokb = ht / S::GRB;
         const int c = cfirst + gr * 4, have = cend - c;
-        const T *px = (const T *)f.x + b * f.xs.b + c, *pdt = (const T *)f.dt + b * f.dts.b + c;
-        const T *pdy = (const T *)a.dy + b * a.dys.b + c;
-        const T *pz = f.z ? (const T *)f.z + b * f.zs.b + c : nullptr;
-        const T *pB = (const T *)f.Bm + b * f.bs.b + (size_t)gi * N + grb * 4;
-        const T *pC = (const T *)f.Cm + b * f.cs.b + (size_t)gi * N + grb * 4;
+        const bool whole = cfirst + S::CB <= cend;
+        auto token_of = [&](int i) { return t0 + (tiles - 1 - i) * kTile; };   // of the i-th tile, from the end
+        // running pointers to this thread's first element of the tile that is fetched next
+        const long long first = (long long)t0 + (tiles ? (long long)(tiles - 1) * kTile : 0);
+        const T *px = (const T *)f.x + b * f.xs.b + c + (first + tok) * f.xs.t;
+        const T *pdt = (const T *)f.dt + b * f.dts.b + c + (first + tok) * f.dts.t;
+        const T *pdy = (const T *)a.dy + b * a.dys.b + c + (first + tok) * a.dys.t;
+        const T *pz = f.z ? (const T *)f.z + b * f.zs.b + c + (first + tok) * f.zs.t : nullptr;
+        const T *pB = (const T *)f.Bm + b * f.bs.b + (size_t)gi * N + grb * 4 + (first + tokb) * f.bs.t;
+        const T *pC = (const T *)f.Cm + b * f.cs.b + (size_t)gi * N + grb * 4 + (first + tokb) * f.cs.t;
         const size_t row = (size_t)b * f.T * f.D + c;
+        size_t out = row + (first + tok) * f.D;               // and of the tile that is finished next
+        float *pbc = parts.bc + ((((size_t)blk * f.B + b) * f.T + first) * f.G + gi) * 2 * N;
         float bias[4], skip[4], sumD[4] = {}, sumb[4] = {};
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             bias[v] = f.dt_bias && v < have ? f.dt_bias[c + v] : 0.f;
             skip[v] = f.D_skip && v < have ? f.D_skip[c + v] : 0.f;
         }
-        struct Set {
-            V x[S::R], dt[S::R], dy[S::R], z[S::R];
-        };
-        Set in, out;
-        V rB[S::RB], rC[S::RB];
-        auto fetch = [&](Set &s, int tile) {
+        V rx[S::R], rdt[S::R], rdy[S::R], rz[S::R], rB[S::RB], rC[S::RB];
+        // what a tile's last step needs of its first, one and two tiles old: x, the slope of the
+        // softplus, and dy silu'(z)
+        struct Kept {
+            V x[S::R];
+            float slope[S::R][4], dz[S::R][4];
+        } old, mid;
+        auto fetch = [&](int i) {
+            const int tb = token_of(i);
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const long long t = (long long)tile * kTile + k;
-                const int valid = k < kTile && t < len ? have : 0;
-                s.x[r] = load4<T, VECTOR>(px + t * f.xs.t, valid);
-                s.dt[r] = load4<T, VECTOR>(pdt + t * f.dts.t, valid);
-                s.dy[r] = load4<T, VECTOR>(pdy + t * a.dys.t, valid);
-                if (pz) s.z[r] = load4<T, VECTOR>(pz + t * f.zs.t, valid);
+                const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
+                rx[r] = load4<T, VECTOR>(px + r * S::TPP * f.xs.t, valid);
+                rdt[r] = load4<T, VECTOR>(pdt + r * S::TPP * f.dts.t, valid);
+                rdy[r] = load4<T, VECTOR>(pdy + r * S::TPP * a.dys.t, valid);
+                if (pz) rz[r] = load4<T, VECTOR>(pz + r * S::TPP * f.zs.t, valid);
             }
-        };
-        auto fetch_bc = [&](int tile) {
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
-                const long long t = (long long)tile * kTile + k;
-                const int valid = k < kTile && t < len ? 4 : 0;
-                rB[r] = load4<T, VECTOR>(pB + t * f.bs.t, valid);
-                rC[r] = load4<T, VECTOR>(pC + t * f.cs.t, valid);
+                const int valid = full && S::TPB <= kTile ? 4 : k < kTile && tb + k < t1 ? 4 : 0;
+                rB[r] = load4<T, VECTOR>(pB + r * S::TPB * f.bs.t, valid);
+                rC[r] = load4<T, VECTOR>(pC + r * S::TPB * f.cs.t, valid);
             }
+            px -= kTile * f.xs.t;
+            pdt -= kTile * f.dts.t;
+            pdy -= kTile * a.dys.t;
+            if (pz) pz -= kTile * f.zs.t;
+            pB -= kTile * f.bs.t;
+            pC -= kTile * f.cs.t;
         };
-        auto prepare = [&](int i) {
+        auto prepare = [&](int i, Kept &keep) {
             float *buf = sm + (i & 1) * S::BUF;
-            const int tile = tiles - 1 - i;
+            const int tb = token_of(i);
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                if (k >= kTile) continue;
-                const bool live = tile * kTile + k < len;
-                float fx[4], fd[4], fy[4], fz[4], dc[4];
-                unpack(in.x[r], fx);
-                unpack(in.dt[r], fd);
-                unpack(in.dy[r], fy);
-                if (pz) unpack(in.z[r], fz);
+                if (S::TPP > kTile && k >= kTile) continue;
+                float fx[4], fd[4], fy[4], fz[4];
+                unpack(rx[r], fx);
+                unpack(rdt[r], fd);
+                unpack(rdy[r], fy);
+                if (pz) unpack(rz[r], fz);
+                keep.x[r] = rx[r];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    float d = fd[v] + bias[v];
-                    if (f.softplus) { float e; d = softplus_f32(d, e); }
-                    if (!live || v >= have) d = 0.f;
-                    const float u = d * fx[v];
-                    dc[v] = pz ? fy[v] * (fz[v] * sigmoid_f32(fz[v])) : fy[v];
-                    *(float4 *)(buf + ((size_t)k * S::CB + swz(gr * 4 + v)) * 4) = make_float4(d, d, u, u);
+                    float e, d = fd[v] + bias[v], slope = 1.f;
+                    if (f.softplus) {
+                        const float pre = d;
+                        d = softplus_f32(pre, e);
+                        const float q = rcp_approx(1.f + e);      // sigmoid(|pre|)
+                        slope = pre < 0.f ? e * q : q;
+                    }
+                    if (!full && (tb + k >= t1 || v >= have)) d = 0.f;
+                    fd[v] = d;
+                    fx[v] *= d;
+                    keep.slope[r][v] = slope;
+                    if (pz) {
+                        const float q = sigmoid_f32(fz[v]), zq = fz[v] * q;
+                        keep.dz[r][v] = fy[v] * fmaf(zq, 1.f - q, q);
+                        fy[v] *= zq;
+                    }
                 }
-                float *q = buf + S::P + (size_t)k * S::CB * 2;
-                *(float4 *)(q + swz(gr * 2) * 4) = make_float4(dc[0], dc[0], dc[1], dc[1]);
-                *(float4 *)(q + swz(gr * 2 + 1) * 4) = make_float4(dc[2], dc[2], dc[3], dc[3]);
+                float *q = buf + k * S::CB * 2;
+                *(float4 *)(q + swz(gr * 2) * 4) = make_float4(fd[0], fx[0], fd[1], fx[1]);
+                *(float4 *)(q + swz(gr * 2 + 1) * 4) = make_float4(fd[2], fx[2], fd[3], fx[3]);
+                *(float4 *)(buf + S::P + k * S::CB + swz(gr) * 4) = make_float4(fy[0], fy[1], fy[2], fy[3]);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
-                if (k >= kTile) continue;
-                float g[4];
-                float *q = buf + S::P + S::DC + k * N + grb * 4;
-                unpack(rB[r], g);
-                *(float4 *)q = make_float4(g[0], g[1], g[2], g[3]);
-                unpack(rC[r], g);
-                *(float4 *)(q + S::S) = make_float4(g[0], g[1], g[2], g[3]);
+                if (S::TPB > kTile && k >= kTile) continue;
+                T *q = (T *)(buf + S::P + S::DC) + k * N + grb * 4;
+                *(V *)q = rB[r];
+                *(V *)(q + kTile * N) = rC[r];
             }
         };
-        auto finish = [&](int i) {
+        auto finish = [&](int i, const Kept &keep) {
             const float *buf = sm + (i & 1) * S::BUF;
             const float *y2 = buf + S::P + S::DC + 2 * S::S, *y1 = y2 + S::Y2, *sq = y1 + S::Y1;
-            const int tile = tiles - 1 - i;
+            const int tb = token_of(i);
+            const bool full = whole && tb + kTile <= t1;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const long long t = (long long)tile * kTile + k;
-                if (k >= kTile || t >= f.T) continue;
-                float gx[4] = {}, gd[4] = {}, gz[4] = {};
-                if (t < len) {
-                    float fx[4], fd[4], fy[4], fz[4];
-                    unpack(out.x[r], fx);
-                    unpack(out.dt[r], fd);
-                    unpack(out.dy[r], fy);
-                    if (pz) unpack(out.z[r], fz);
+                if (S::TPP > kTile && k >= kTile) continue;
+                if (!full && tb + k >= stop) continue;
+                const bool live = full || tb + k < t1;
+                // this thread's own entries of the buffer
+                const float *q = buf + k * S::CB * 2;
+                const float4 d01 = *(const float4 *)(q + swz(gr * 2) * 4), d23 = *(const float4 *)(q + swz(gr * 2 + 1) * 4);
+                const float4 dc4 = *(const float4 *)(buf + S::P + k * S::CB + swz(gr) * 4);
+                const float delta[4] = {d01.x, d01.z, d23.x, d23.z}, dc[4] = {dc4.x, dc4.y, dc4.z, dc4.w};
+                float fx[4], gx[4], gd[4], gz[4];
+                unpack(keep.x[r], fx);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int s0 = (gr * 4 + v) * S::LN;      // LN partial sums of the channel
-                        float du = 0.f, sw = 0.f, sy = 0.f;
+                for (int v = 0; v < 4; ++v) {
+                    const int s0 = (gr * 4 + v) * S::LN;          // LN partial sums of the channel
+                    float du = 0.f, sw = 0.f, sy = 0.f;
 #pragma unroll
-                        for (int q = 0; q < S::LN / 2; ++q) {
-                            const float4 w =
-                                *(const float4 *)(y2 + (size_t)k * kLanes * 4 + swz((s0 >> 1) + q) * 4);
-                            du += w.x + w.z;
-                            sw += w.y + w.w;
-                        }
-                        if (pz) {
-                            if (S::LN >= 4) {
+                    for (int l = 0; l < S::LN / 2; ++l) {
+                        const float4 w = *(const float4 *)(y2 + k * kLanes * 4 + swz((s0 >> 1) + l) * 4);
+                        du += w.x + w.z;
+                        sw += w.y + w.w;
+                    }
+                    gx[v] = fmaf(du, delta[v], dc[v] * skip[v]);
+                    gd[v] = fmaf(du, fx[v], sw * 0.6931471805599453f) * keep.slope[r][v];
+                    if (pz) {
+                        if (S::LN >= 4) {
 #pragma unroll
-                                for (int q = 0; q < S::LN / 4; ++q) {
-                                    const float4 w =
-                                        *(const float4 *)(y1 + (size_t)k * kLanes * 2 + swz((s0 >> 2) + q) * 4);
-                                    sy += (w.x + w.y) + (w.z + w.w);
-                                }
-                            } else {
-                                const float2 w = *(const float2 *)(y1 + (size_t)k * kLanes * 2 +
-                                                                   swz(s0 >> 2) * 4 + (s0 & 3));
-                                sy = w.x + w.y;
+                            for (int l = 0; l < S::LN / 4; ++l) {
+                                const float4 w = *(const float4 *)(y1 + k * kLanes * 2 + swz((s0 >> 2) + l) * 4);
+                                sy += (w.x + w.y) + (w.z + w.w);
                             }
+                        } else {
+                            const float2 w = *(const float2 *)(y1 + k * kLanes * 2 + swz(s0 >> 2) * 4 + (s0 & 3));
+                            sy = w.x + w.y;
                         }
-                        const float pre = fd[v] + bias[v];
-                        float e2; const float delta = f.softplus ? softplus_f32(pre, e2) : pre;
-                        float dc = fy[v];
-                        if (pz) {
-                            const float s = sigmoid_f32(fz[v]);
-                            dc = fy[v] * (fz[v] * s);
-                            gz[v] = fy[v] * fmaf(skip[v], fx[v], sy) * fmaf(fz[v] * s, 1.f - s, s);
-                        }
-                        gx[v] = fmaf(du, delta, dc * skip[v]);
-                        float dd = fmaf(du, fx[v], sw * 0.6931471805599453f);
-                        if (f.softplus) dd *= sigmoid_f32(pre);
-                        gd[v] = dd;
-                        if (v < have) {
-                            sumD[v] = fmaf(dc, fx[v], sumD[v]);
-                            sumb[v] += dd;
-                        }
+                        gz[v] = keep.dz[r][v] * fmaf(skip[v], fx[v], sy);
+                    }
+                    if (!live) gx[v] = gd[v] = gz[v] = 0.f;
+                    if (full || (live && v < have)) {
+                        sumD[v] = fmaf(dc[v], fx[v], sumD[v]);
+                        sumb[v] += gd[v];
                     }
                 }
-                store4<T, VECTOR>((T *)a.dx + row + t * f.D, gx, have);
-                store4<T, VECTOR>((T *)a.ddt + row + t * f.D, gd, have);
-                if (pz) store4<T, VECTOR>((T *)a.dz + row + t * f.D, gz, have);
+                const size_t o = out + (size_t)(r * S::TPP) * f.D;
+                const int n = full ? 4 : have;
+                store4<T, VECTOR>((T *)a.dx + o, gx, n);
+                store4<T, VECTOR>((T *)a.ddt + o, gd, n);
+                if (pz) store4<T, VECTOR>((T *)a.dz + o, gz, n);
             }
+            out -= (size_t)kTile * f.D;
             // the four warps' sums of dB and dC
-            for (int q = ht; q < kTile * N / 2; q += kLanes) {
-                const int k = q / (N / 2), e = (q - k * (N / 2)) * 4;
-                const long long t = (long long)tile * kTile + k;
-                if (t >= len) continue;
-                float4 s = *(const float4 *)(sq + (size_t)k * 8 * N + e);
+#pragma unroll
+            for (int q = 0; q < kTile * N / 2; q += kHelpers) {
+                const int j = q + ht, k = j / (N / 2), e = (j - k * (N / 2)) * 4;
+                if ((kTile * N / 2 < kHelpers && j >= kTile * N / 2) || tb + k >= t1) continue;
+                float4 s = *(const float4 *)(sq + k * 8 * N + e);
 #pragma unroll
                 for (int w = 1; w < 4; ++w) {
-                    const float4 m = *(const float4 *)(sq + ((size_t)k * 4 + w) * 2 * N + e);
+                    const float4 m = *(const float4 *)(sq + (k * 4 + w) * 2 * N + e);
                     s.x += m.x;
                     s.y += m.y;
                     s.z += m.z;
                     s.w += m.w;
                 }
-                *(float4 *)(parts.bc + ((((size_t)blk * f.B + b) * f.T + t) * f.G + gi) * 2 * N + e) = s;
+                *(float4 *)(pbc + (size_t)k * f.G * 2 * N + e) = s;
             }
+            pbc -= (size_t)kTile * f.G * 2 * N;
         };
 
         // behind the row's end the gradients are zero
         const float zero[4] = {};
-        for (long long t = (long long)tiles * kTile + tok; t < f.T; t += S::TPP) {
+        for (long long t = (long long)t0 + tiles * kTile + tok; t < stop; t += S::TPP) {
             store4<T, VECTOR>((T *)a.dx + row + t * f.D, zero, have);
             store4<T, VECTOR>((T *)a.ddt + row + t * f.D, zero, have);
             if (pz) store4<T, VECTOR>((T *)a.dz + row + t * f.D, zero, have);
         }
         if (tiles) {
-            fetch(in, tiles - 1);
-            fetch_bc(tiles - 1);
-            prepare(0);
-            if (tiles > 1) {
-                fetch(in, tiles - 2);
-                fetch_bc(tiles - 2);
-            }
+            fetch(0);
+            prepare(0, mid);
+            if (tiles > 1) fetch(1);
         }
         __syncthreads();
         for (int i = 0; i < tiles; ++i) {
-            if (i + 1 < tiles) prepare(i + 1);
-            if (i + 2 < tiles) {
-                fetch(in, tiles - 3 - i);
-                fetch_bc(tiles - 3 - i);
-            }
-            if (i > 0) finish(i - 1);
-            fetch(out, tiles - 1 - i);
+            if (i > 0) finish(i - 1, old);     // ahead of the entries' next use
+            old = mid;
+            if (i + 1 < tiles) prepare(i + 1, mid);
+            if (i + 2 < tiles) fetch(i + 2);
             __syncthreads();
         }
-        if (tiles) finish(tiles - 1);
+        if (tiles) finish(tiles - 1, old);
         // the walk is over: its shared memory takes the helpers' sums over tokens, and only they meet
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
         float *red = sm;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             red[(tok * S::CB + gr * 4 + v) * 2] = sumD[v];
             red[(tok * S::CB + gr * 4 + v) * 2 + 1] = sumb[v];
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        for (int k = ht; k < S::CB; k += kLanes)
+        asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
+        for (int k = ht; k < S::CB; k += kHelpers)
             if (cfirst + k < cend) {
                 float d = 0.f, m = 0.f;
                 for (int q = 0; q < S::TPP; ++q) {
                     d += red[(q * S::CB + k) * 2];
                     m += red[(q * S::CB + k) * 2 + 1];
                 }
-                parts.dD[(size_t)b * f.D + cfirst + k] = d;
-                parts.dbias[(size_t)b * f.D + cfirst + k] = m;
+                parts.dD[row_of_parts * f.D + cfirst + k] = d;
+                parts.dbias[row_of_parts * f.D + cfirst + k] = m;
             }
     }
 }
@@ -501,7 +555,7 @@ ssm_bwd_sum_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_gro
     }
     if (!o) return;
     float s = 0.f;
-    for (int b = 0; b < f.B; ++b) s += p[(size_t)b * stride];
+    for (int b = 0; b < f.B * parts.pc.count; ++b) s += p[(size_t)b * stride];
     *o = s;
 }
 
@@ -511,12 +565,29 @@ int blocks_per_group(int D, int G, int N)
     return (D / G + cb - 1) / cb;
 }
 
+// As in the forward: few channels, then pieces side by side.  A piece's
+// gradient from behind costs another pass of exponentials (about a third of
+// the walk), so it pays from half the machine down.
+BackPieces plan(int B, int T, int D, int G, int N)
+{
+    BackPieces p = {1, T > 0 ? T : 1, nullptr, nullptr};
+    const long long blocks = (long long)B * G * blocks_per_group(D, G, N);
+    if (blocks > 0 && blocks * 2 <= kSms && T >= 256) {
+        long long count = kSms / blocks;
+        if (count > T / 128) count = T / 128;
+        p.tokens = (int)((T + count - 1) / count + 31) / 32 * 32;
+        p.count = (T + p.tokens - 1) / p.tokens;
+    }
+    return p;
+}
+
 struct Layout {
-    size_t points, bc, dA, dD, scan, total;   // offsets in bytes, 256-byte steps
+    size_t points, bc, dA, dD, slots, sums, scan, total;   // offsets in bytes, 256-byte steps
 };
 Layout layout(int B, int T, int D, int G, int N)
 {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t pieces = plan(B, T, D, G, N).count;
     Layout l;
     size_t at = 0;
     l.points = at;
@@ -524,9 +595,13 @@ Layout layout(int B, int T, int D, int G, int N)
     l.bc = at;
     at += up((size_t)blocks_per_group(D, G, N) * B * T * G * 2 * N * 4);
     l.dA = at;
-    at += up((size_t)B * D * N * 4);
+    at += up(pieces * B * D * N * 4);
     l.dD = at;
-    at += up((size_t)B * D * 2 * 4);
+    at += up(pieces * B * D * 2 * 4);
+    l.slots = at;
+    at += pieces > 1 ? up(pieces * B * D * N * 4) : 0;
+    l.sums = at;
+    at += pieces > 1 ? up(pieces * B * D * 4) : 0;
     l.scan = at;
     l.total = at + ssm_scan_fwd_workspace_bytes(B, T, D, G, N);
     return l;
@@ -548,11 +623,12 @@ template <typename T> bool bwd_vectors(const ScanBwdArgs &a)
 template <typename T, int N, bool VECTOR>
 cudaError_t run_bwd(const ScanBwdArgs &a, const BwdParts &p, cudaStream_t st)
 {
+    using S = Shape<T, N>;
     auto k = ssm_bwd_kernel<T, N, VECTOR>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<N>::smem);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
     if (e != cudaSuccess) return e;
     const int bpg = blocks_per_group(a.f.D, a.f.G, N);
-    k<<<(unsigned)((long long)a.f.B * a.f.G * bpg), kThreads, Shape<N>::smem, st>>>(a, p, bpg);
+    k<<<dim3((unsigned)((long long)a.f.B * a.f.G * bpg), p.pc.count), kThreads, S::smem, st>>>(a, p, bpg);
     return cudaGetLastError();
 }
 
@@ -582,7 +658,10 @@ cudaError_t launch_ssm_scan_bwd(const ScanBwdArgs &a, cudaStream_t stream, int *
     p.bc = (float *)(ws + l.bc);
     p.dA = (float *)(ws + l.dA);
     p.dD = (float *)(ws + l.dD);
-    p.dbias = p.dD + (size_t)f.B * f.D;
+    p.pc = plan(f.B, f.T, f.D, f.G, f.N);
+    p.pc.slots = (float *)(ws + l.slots);
+    p.pc.sums = (float *)(ws + l.sums);
+    p.dbias = p.dD + (size_t)p.pc.count * f.B * f.D;
     cudaError_t e;
     if (f.T > 0) {
         ScanArgs s = f;
@@ -590,6 +669,17 @@ cudaError_t launch_ssm_scan_bwd(const ScanBwdArgs &a, cudaStream_t stream, int *
         s.z = nullptr;
         s.workspace = ws + l.scan;
         e = launch_ssm_scan_checkpoints(s, p.points, stream, launches);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.pc.count > 1) {
+        ScanArgs s = f;
+        s.x = a.dy;
+        s.xs = a.dys;
+        s.Bm = f.Cm;
+        s.bs = f.cs;
+        s.D_skip = s.h0 = nullptr;
+        s.y = nullptr;
+        e = launch_ssm_scan_adjoint(s, p.pc.count, p.pc.tokens, p.pc.slots, p.pc.sums, stream, launches);
         if (e != cudaSuccess) return e;
     }
     e = f.bf16 ? bwd_typed<__nv_bfloat16>(a, p, stream) : bwd_typed<float>(a, p, stream);

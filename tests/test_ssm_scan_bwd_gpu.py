@@ -45,6 +45,9 @@ CASES = [
     dict(B=2, T=90, D=288, N=16, G=4, dt=FP, state=False),           # blocks end inside a group
     dict(B=4, T=40, D=8, N=32, G=2, lengths=[-3, 99, 8, 39]),
     dict(B=1, T=400, D=40, N=16),                                    # pieces of a row
+    dict(B=3, T=520, D=20, N=8, G=2, dt=FP, lengths=[520, 130, 0]),
+    dict(B=2, T=300, D=18, N=32, lengths=[160, 161]),                # a row that ends with a piece
+    dict(B=1, T=270, D=12, N=64, z=False),
     dict(B=2, T=0, D=16, N=16),
 ]
 
