@@ -17,10 +17,10 @@
 //
 // Issue slots bound the walk: per (token, channel, state) it takes the sums
 // over n (three), over the channels (two) and over tokens (one).  A thread
-// owns 4 states of 2 channels: sums over n start in the thread and end with
-// the helper warps (through shared memory), sums over channels start in the
-// thread and go through the warp by an exchange that halves the number of
-// values at each step.  Blocks' parts of dB and dC, and batch rows' parts of
+// owns 4 states of a channel: sums over n start in the thread and end with
+// the helper warps (through shared memory), sums over channels go through the
+// warp by an exchange that halves the number of values at each step and end
+// with the helpers too.  Blocks' parts of dB and dC, and batch rows' parts of
 // dA, dD and ddt_bias, are added by a last kernel in a fixed order: no atomics,
 // equal calls give equal bits.
 #include "ssm_internal.cuh"
@@ -29,21 +29,21 @@ namespace gdr {
 namespace {
 
 constexpr int kSms = 148;
-constexpr int kLanes = 128;              // threads that walk: 4 states x 2 channels each
+constexpr int kLanes = 256;              // threads that walk: 4 states of a channel each
 constexpr int kHelpers = 256;            // threads that load, form the time steps and write the results
 constexpr int kThreads = kLanes + kHelpers;
-constexpr int kTile = 16;                // tokens between two block barriers
+constexpr int kWarps = kLanes / 32;
 constexpr int kSub = kCheckpoint;        // tokens recomputed at a time
-// Registers a thread: the launch gives every thread 168; the walk keeps 8
-// tokens' decays and states and takes 240, which the helpers make room for
-// (128 * 240 + 256 * 128 = 63488 <= 384 * 168 = 64512).
-constexpr int kWalkRegs = 240, kHelperRegs = 128;
+// Registers a thread: the launch gives every thread 128; the walk keeps 8
+// tokens' decays and states and takes 144, which the helpers make room for
+// (256 * 144 + 256 * 112 = 512 * 128).
+constexpr int kWalkRegs = 144, kHelperRegs = 112;
 
 template <typename T, int N> struct Shape {
     static constexpr int LN = N / 4;                   // lanes of a channel
-    static constexpr int CL = 32 / LN;                 // pairs of channels side by side in a warp
-    static constexpr int CW = 2 * CL;                  // channels of a warp
-    static constexpr int CB = 4 * CW;                  // channels of a block
+    static constexpr int CL = 32 / LN;                 // channels of a warp
+    static constexpr int CB = kWarps * CL;             // channels of a block
+    static constexpr int kTile = N == 64 ? 8 : 16;     // tokens between two block barriers
     static constexpr int GR = CB / 4;
     static constexpr int TPP = kHelpers / GR;
     static constexpr int R = TPP >= kTile ? 1 : kTile / TPP;
@@ -54,9 +54,9 @@ template <typename T, int N> struct Shape {
     static constexpr int P = kTile * CB * 2;           // {delta, u}
     static constexpr int DC = kTile * CB;              // dc
     static constexpr int S = kTile * N * sizeof(T) / 4;   // B, then C, in the inputs' type
-    static constexpr int Y2 = kTile * 2 * kLanes * 2;  // {du, sum w A2} of each lane and channel
-    static constexpr int Y1 = kTile * 2 * kLanes;      // C h of each lane and channel
-    static constexpr int Q = kTile * 4 * 2 * N;        // the warps' sums of dB and dC
+    static constexpr int Y2 = kTile * kLanes * 2;      // {du, sum w A2} of each lane
+    static constexpr int Y1 = kTile * kLanes;          // C h of each lane
+    static constexpr int Q = kTile * kWarps * 2 * N;   // the warps' sums of dB and dC
     static constexpr int BUF = P + DC + 2 * S + Y2 + Y1 + Q;
     static constexpr size_t smem = 2 * BUF * sizeof(float);
 };
@@ -112,6 +112,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
 {
     using S = Shape<T, N>;
     using V = typename Pack<T, 4>::V;
+    constexpr int kTile = S::kTile;
     extern __shared__ __align__(16) float sm[];
     const ScanArgs &f = a.f;
     const BackPieces &pc = parts.pc;
@@ -135,153 +136,118 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWalkRegs));
         const int warp = tid >> 5, lane = tid & 31;
         const int ln = lane % S::LN, n0 = ln * 4;
-        const int ch = warp * S::CW + lane / S::LN * 2;       // and ch + 1
-        const size_t at = ((size_t)b * f.D + cfirst + ch) * N + n0;
-        bool on[2];
-        f32x2 A[2][2], carry[2][2], dA[2][2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            on[k] = cfirst + ch + k < cend;
-            float4 q = make_float4(0.f, 0.f, 0.f, 0.f), r = q;
-            if (on[k]) {
-                q = *(const float4 *)(f.A + (size_t)(cfirst + ch + k) * N + n0);
-                if (a.dh_T) r = *(const float4 *)(a.dh_T + at + k * N);
-            }
-            A[k][0] = make_f32x2(q.x * kLog2e, q.y * kLog2e);
-            A[k][1] = make_f32x2(q.z * kLog2e, q.w * kLog2e);
-            carry[k][0] = make_f32x2(r.x, r.y);
-            carry[k][1] = make_f32x2(r.z, r.w);
-            dA[k][0] = dA[k][1] = 0;
-            // fold in the pieces behind, the last that the row has first
-            if (pc.count > 1 && on[k])
-                for (int s = (len - 1) / pc.tokens; s > piece; --s) {
-                    const f32x2 sum = both(pc.sums[((size_t)s * f.B + b) * f.D + cfirst + ch + k]);
-                    const ulonglong2 v = *(const ulonglong2 *)(pc.slots + (size_t)s * f.B * f.D * N + at + k * N);
-                    carry[k][0] = fma2(decay2(sum, A[k][0]), carry[k][0], v.x);
-                    carry[k][1] = fma2(decay2(sum, A[k][1]), carry[k][1], v.y);
-                }
+        const int ch = warp * S::CL + lane / S::LN, c = cfirst + ch;
+        const bool on = c < cend;
+        const size_t at = ((size_t)b * f.D + c) * N + n0;
+        float4 q4 = make_float4(0.f, 0.f, 0.f, 0.f), r4 = q4;
+        if (on) {
+            q4 = *(const float4 *)(f.A + (size_t)c * N + n0);
+            if (a.dh_T) r4 = *(const float4 *)(a.dh_T + at);
         }
-        // the stored states ahead of the sub-tile that comes next
+        const f32x2 A0 = make_f32x2(q4.x * kLog2e, q4.y * kLog2e), A1 = make_f32x2(q4.z * kLog2e, q4.w * kLog2e);
+        f32x2 carry0 = make_f32x2(r4.x, r4.y), carry1 = make_f32x2(r4.z, r4.w), dA0 = 0, dA1 = 0;
+        // fold in the pieces behind, the last that the row has first
+        if (pc.count > 1 && on)
+            for (int s = (len - 1) / pc.tokens; s > piece; --s) {
+                const f32x2 sum = both(pc.sums[((size_t)s * f.B + b) * f.D + c]);
+                const ulonglong2 v = *(const ulonglong2 *)(pc.slots + (size_t)s * f.B * f.D * N + at);
+                carry0 = fma2(decay2(sum, A0), carry0, v.x);
+                carry1 = fma2(decay2(sum, A1), carry1, v.y);
+            }
+        // the stored state ahead of the sub-tile that comes next
         const size_t pstride = (size_t)f.D * N;
-        const float *point = parts.points + ((size_t)b * ((f.T + kSub - 1) / kSub) * f.D + cfirst + ch) * N + n0;
-        ulonglong2 state[2] = {make_ulonglong2(0, 0), make_ulonglong2(0, 0)};
+        const float *point = parts.points + ((size_t)b * ((f.T + kSub - 1) / kSub) * f.D + c) * N + n0;
+        ulonglong2 state = make_ulonglong2(0, 0);
         auto fetch_state = [&](int t) {
-            if (t >= t0 && t < t1)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (on[k]) state[k] = *(const ulonglong2 *)(point + (size_t)(t / kSub) * pstride + k * N);
+            if (t >= t0 && t < t1 && on) state = *(const ulonglong2 *)(point + (size_t)(t / kSub) * pstride);
         };
         fetch_state(t0 + tiles * kTile - kSub);
         __syncthreads();
         for (int i = 0; i < tiles; ++i) {
             const int tb0 = t0 + (tiles - 1 - i) * kTile;
             float *buf = sm + (i & 1) * S::BUF;
-            const float *p = buf + swz(ch >> 1) * 4, *pd = buf + S::P + swz(ch >> 2) * 4 + (ch & 2);
+            const float *p = buf + swz(ch >> 1) * 4 + (ch & 1) * 2, *pd = buf + S::P + swz(ch >> 2) * 4 + (ch & 3);
             const T *sB = (const T *)(buf + S::P + S::DC) + n0, *sC = (const T *)(buf + S::P + S::DC + S::S) + n0;
             float *y2 = buf + S::P + S::DC + 2 * S::S, *y1 = y2 + S::Y2;
             float *sq = y1 + S::Y1 + warp * 2 * N + n0;
-            float *o2[2], *o1[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int s = (ch + k) * S::LN + ln;
-                o2[k] = y2 + swz(s >> 1) * 4 + (s & 1) * 2;
-                o1[k] = y1 + swz(s >> 2) * 4 + (s & 3);
-            }
+            float *o2 = y2 + swz(tid >> 1) * 4 + (tid & 1) * 2, *o1 = y1 + swz(tid >> 2) * 4 + (tid & 3);
 #pragma unroll 1
             for (int sub = kTile / kSub - 1; sub >= 0; --sub) {
                 const int tb = sub * kSub;
-                f32x2 av[kSub][2][2], hv[kSub + 1][2][2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    hv[0][k][0] = state[k].x;
-                    hv[0][k][1] = state[k].y;
-                }
+                f32x2 a0[kSub], a1[kSub], h0[kSub + 1], h1[kSub + 1];
+                h0[0] = state.x;
+                h1[0] = state.y;
                 // A sub-tile behind the row's end has no stored state (it is 0 then); its tokens
                 // have delta = dc = 0 and change nothing.
                 fetch_state(tb0 + tb - kSub);
 #pragma unroll
                 for (int t = 0; t < kSub; ++t) {
-                    const float4 du = *(const float4 *)(p + (tb + t) * S::CB * 2);
+                    const float2 du = *(const float2 *)(p + (tb + t) * S::CB * 2);
                     const Quad<T> bq = *(const Quad<T> *)(sB + (tb + t) * N);
-                    const f32x2 b0 = bq.lo(), b1 = bq.hi();
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const f32x2 d = both(k ? du.z : du.x), u = both(k ? du.w : du.y);
-                        av[t][k][0] = decay2(d, A[k][0]);
-                        av[t][k][1] = decay2(d, A[k][1]);
-                        hv[t + 1][k][0] = fma2(av[t][k][0], hv[t][k][0], mul2(u, b0));
-                        hv[t + 1][k][1] = fma2(av[t][k][1], hv[t][k][1], mul2(u, b1));
-                    }
+                    const f32x2 d = both(du.x), u = both(du.y);
+                    a0[t] = decay2(d, A0);
+                    a1[t] = decay2(d, A1);
+                    h0[t + 1] = fma2(a0[t], h0[t], mul2(u, bq.lo()));
+                    h1[t + 1] = fma2(a1[t], h1[t], mul2(u, bq.hi()));
                 }
-                // A token's operands are loaded ahead of the stores of the token before it.
+                // A token's operands are loaded while the one before is in work, and its sums and
+                // stores wait until the next one's work is under way: loads stay behind stores, and
+                // stores behind the exchange between the lanes, which takes about 100 cycles.
                 struct Token {
-                    float4 du;
-                    float2 dc;
+                    float2 du;
+                    float dc;
                     Quad<T> b, c;
                 } now, next;
+                struct Sums {
+                    float v[8], su, sw, sy;
+                } done;
                 auto fetch = [&](Token &k, int t) {
-                    k.du = *(const float4 *)(p + t * S::CB * 2);
-                    k.dc = *(const float2 *)(pd + t * S::CB);
+                    k.du = *(const float2 *)(p + t * S::CB * 2);
+                    k.dc = pd[t * S::CB];
                     k.b = *(const Quad<T> *)(sB + t * N);
                     k.c = *(const Quad<T> *)(sC + t * N);
+                };
+                auto store = [&](Sums &k, int t) {
+                    int which = 0;
+                    lane_sums<8, S::LN>(k.v, lane, which);
+                    *(float2 *)(o2 + t * kLanes * 2) = make_float2(k.su, k.sw);
+                    if (f.z) o1[t * kLanes] = k.sy;
+                    constexpr int left = 8 / S::CL > 1 ? 8 / S::CL : 1;
+                    if (S::CL <= 8 || lane < 16) {
+                        float *o = sq + t * kWarps * 2 * N + (which >> 2) * N + (which & 3);
+#pragma unroll
+                        for (int j = 0; j < left; ++j) o[j] = k.v[j];
+                    }
                 };
                 fetch(now, tb + kSub - 1);
 #pragma unroll
                 for (int t = kSub - 1; t >= 0; --t) {
                     if (t > 0) fetch(next, tb + t - 1);
-                    const f32x2 b0 = now.b.lo(), b1 = now.b.hi(), c0 = now.c.lo(), c1 = now.c.hi();
-                    f32x2 dB0, dB1, dC0, dC1;
-                    float su[2], sw[2], sy[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const f32x2 d = both(k ? now.du.z : now.du.x), u = both(k ? now.du.w : now.du.y);
-                        const f32x2 dc = both(k ? now.dc.y : now.dc.x);
-                        const f32x2 g0 = fma2(dc, c0, carry[k][0]), g1 = fma2(dc, c1, carry[k][1]);
-                        dB0 = k ? fma2(g0, u, dB0) : mul2(g0, u);
-                        dB1 = k ? fma2(g1, u, dB1) : mul2(g1, u);
-                        dC0 = k ? fma2(dc, hv[t + 1][k][0], dC0) : mul2(dc, hv[t + 1][k][0]);
-                        dC1 = k ? fma2(dc, hv[t + 1][k][1], dC1) : mul2(dc, hv[t + 1][k][1]);
-                        const f32x2 pu = fma2(g1, b1, mul2(g0, b0));
-                        carry[k][0] = mul2(av[t][k][0], g0);
-                        carry[k][1] = mul2(av[t][k][1], g1);
-                        const f32x2 w0 = mul2(carry[k][0], hv[t][k][0]), w1 = mul2(carry[k][1], hv[t][k][1]);
-                        const f32x2 pw = fma2(w1, A[k][1], mul2(w0, A[k][0]));
-                        dA[k][0] = fma2(w0, d, dA[k][0]);
-                        dA[k][1] = fma2(w1, d, dA[k][1]);
-                        su[k] = lo_f32(pu) + hi_f32(pu);
-                        sw[k] = lo_f32(pw) + hi_f32(pw);
-                        if (f.z) {
-                            const f32x2 y = fma2(hv[t + 1][k][1], c1, mul2(hv[t + 1][k][0], c0));
-                            sy[k] = lo_f32(y) + hi_f32(y);
-                        }
-                    }
-                    float v[8] = {lo_f32(dB0), hi_f32(dB0), lo_f32(dB1), hi_f32(dB1),
-                                  lo_f32(dC0), hi_f32(dC0), lo_f32(dC1), hi_f32(dC1)};
-                    int which = 0;
-                    lane_sums<8, S::LN>(v, lane, which);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        *(float2 *)(o2[k] + (tb + t) * kLanes * 4) = make_float2(su[k], sw[k]);
-                        if (f.z) o1[k][(tb + t) * kLanes * 2] = sy[k];
-                    }
-                    constexpr int left = 8 / S::CL > 1 ? 8 / S::CL : 1;
-                    if (S::CL <= 8 || lane < 16) {
-                        float *o = sq + (tb + t) * 8 * N + (which >> 2) * N + (which & 3);
-#pragma unroll
-                        for (int j = 0; j < left; ++j) o[j] = v[j];
-                    }
+                    const f32x2 d = both(now.du.x), u = both(now.du.y), dc = both(now.dc);
+                    const f32x2 c0 = now.c.lo(), c1 = now.c.hi();
+                    const f32x2 g0 = fma2(dc, c0, carry0), g1 = fma2(dc, c1, carry1);
+                    const f32x2 dB0 = mul2(g0, u), dB1 = mul2(g1, u), dC0 = mul2(dc, h0[t + 1]), dC1 = mul2(dc, h1[t + 1]);
+                    const f32x2 pu = fma2(g1, now.b.hi(), mul2(g0, now.b.lo()));
+                    carry0 = mul2(a0[t], g0);
+                    carry1 = mul2(a1[t], g1);
+                    const f32x2 w0 = mul2(carry0, h0[t]), w1 = mul2(carry1, h1[t]);
+                    const f32x2 pw = fma2(w1, A1, mul2(w0, A0));
+                    dA0 = fma2(w0, d, dA0);
+                    dA1 = fma2(w1, d, dA1);
+                    const f32x2 y = fma2(h1[t + 1], c1, mul2(h0[t + 1], c0));
+                    if (t < kSub - 1) store(done, tb + t + 1);
+                    done = {{lo_f32(dB0), hi_f32(dB0), lo_f32(dB1), hi_f32(dB1), lo_f32(dC0), hi_f32(dC0), lo_f32(dC1),
+                             hi_f32(dC1)}, lo_f32(pu) + hi_f32(pu), lo_f32(pw) + hi_f32(pw), lo_f32(y) + hi_f32(y)};
                     now = next;
                 }
+                store(done, tb);
             }
             __syncthreads();
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (on[k]) {
-                *(ulonglong2 *)(parts.dA + row_of_parts * f.D * N + (size_t)(cfirst + ch + k) * N + n0) =
-                    make_ulonglong2(dA[k][0], dA[k][1]);
-                if (a.dh0 && piece == 0) *(ulonglong2 *)(a.dh0 + at + k * N) = make_ulonglong2(carry[k][0], carry[k][1]);
-            }
+        if (on) {
+            *(ulonglong2 *)(parts.dA + (row_of_parts * f.D + c) * N + n0) = make_ulonglong2(dA0, dA1);
+            if (a.dh0 && piece == 0) *(ulonglong2 *)(a.dh0 + at) = make_ulonglong2(carry0, carry1);
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHelperRegs));
         const int ht = tid - kLanes;
@@ -411,7 +377,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                     float du = 0.f, sw = 0.f, sy = 0.f;
 #pragma unroll
                     for (int l = 0; l < S::LN / 2; ++l) {
-                        const float4 w = *(const float4 *)(y2 + k * kLanes * 4 + swz((s0 >> 1) + l) * 4);
+                        const float4 w = *(const float4 *)(y2 + k * kLanes * 2 + swz((s0 >> 1) + l) * 4);
                         du += w.x + w.z;
                         sw += w.y + w.w;
                     }
@@ -421,11 +387,11 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                         if (S::LN >= 4) {
 #pragma unroll
                             for (int l = 0; l < S::LN / 4; ++l) {
-                                const float4 w = *(const float4 *)(y1 + k * kLanes * 2 + swz((s0 >> 2) + l) * 4);
+                                const float4 w = *(const float4 *)(y1 + k * kLanes + swz((s0 >> 2) + l) * 4);
                                 sy += (w.x + w.y) + (w.z + w.w);
                             }
                         } else {
-                            const float2 w = *(const float2 *)(y1 + k * kLanes * 2 + swz(s0 >> 2) * 4 + (s0 & 3));
+                            const float2 w = *(const float2 *)(y1 + k * kLanes + swz(s0 >> 2) * 4 + (s0 & 3));
                             sy = w.x + w.y;
                         }
                         gz[v] = keep.dz[r][v] * fmaf(skip[v], fx[v], sy);
@@ -443,15 +409,15 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                 if (pz) store4<T, VECTOR>((T *)a.dz + o, gz, n);
             }
             out -= (size_t)kTile * f.D;
-            // the four warps' sums of dB and dC
+            // the warps' sums of dB and dC
 #pragma unroll
             for (int q = 0; q < kTile * N / 2; q += kHelpers) {
                 const int j = q + ht, k = j / (N / 2), e = (j - k * (N / 2)) * 4;
                 if ((kTile * N / 2 < kHelpers && j >= kTile * N / 2) || tb + k >= t1) continue;
-                float4 s = *(const float4 *)(sq + k * 8 * N + e);
+                float4 s = *(const float4 *)(sq + k * kWarps * 2 * N + e);
 #pragma unroll
-                for (int w = 1; w < 4; ++w) {
-                    const float4 m = *(const float4 *)(sq + (k * 4 + w) * 2 * N + e);
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 m = *(const float4 *)(sq + (k * kWarps + w) * 2 * N + e);
                     s.x += m.x;
                     s.y += m.y;
                     s.z += m.z;
