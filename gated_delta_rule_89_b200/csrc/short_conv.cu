@@ -13,6 +13,8 @@
 // layout allows) and walks a run of tokens with the last W-1 rows in
 // registers; neighbouring threads own neighbouring channels, so every access
 // of a warp is one contiguous run of a token row.
+#include <type_traits>
+
 #include "ssm_internal.cuh"
 
 namespace gdr {
@@ -20,6 +22,31 @@ namespace {
 
 constexpr int kConvThreads = 128;
 constexpr int kSms = 148;
+
+// The W taps of VEC neighbouring channels, and their biases.
+template <int VEC, int W>
+__device__ __forceinline__ void load_taps(const float *weight, const float *bias, int c0, float (&w)[W][VEC],
+                                          float (&b)[VEC])
+{
+    const float *p = weight + (size_t)c0 * W;
+    if (W == 4 && (reinterpret_cast<uintptr_t>(weight) & 15) == 0) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float4 q = *(const float4 *)(p + v * W);
+            w[0][v] = q.x;
+            w[1][v] = q.y;
+            w[2 < W ? 2 : 0][v] = q.z;
+            w[3 < W ? 3 : 0][v] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][v] = p[v * W + j];
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) b[v] = bias ? bias[c0 + v] : 0.f;
+}
 
 // blockDim.x channel vectors by blockDim.y token runs; grid.x counts (batch,
 // run) pairs, grid.y channel vectors.
@@ -31,11 +58,11 @@ struct ConvGrid {
 // The run length: long enough that the W-1 rows read again at its start (and,
 // backward, at its end) cost little, short enough that small problems still
 // spread over the machine.
-ConvGrid conv_grid(int B, int T, long long vectors, int threads_per_sm, int longest)
+ConvGrid conv_grid(int B, int T, long long vectors, int widest, int threads_per_sm, int longest)
 {
     ConvGrid g;
     int bx = 1;
-    while (bx < kConvThreads && bx < vectors) bx *= 2;
+    while (bx < widest && bx < vectors) bx *= 2;
     // whole warps along the channels; drop to 32 where a wider block would idle on the last vectors
     while (bx > 32 && (vectors + bx - 1) / bx * bx - vectors >= 32) bx /= 2;
     g.block = dim3(bx, kConvThreads / bx);
@@ -53,7 +80,8 @@ template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int run, int runs)
 {
     using V = typename Pack<T, VEC>::V;
-    constexpr int U = VEC > 1 ? 8 : 16;   // rows loaded ahead
+    // rows in work; as many more are on their way from memory meanwhile
+    constexpr int U = VEC * sizeof(T) > 8 ? 4 : 8;
     const int D = a.H * a.d;
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
     const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -90,29 +118,30 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
             *(V *)(so + (size_t)i * D) = v;
         }
     }
-    const int t1 = min(t0 + run, len);
-    if (t0 >= t1) return;
-
-    float w[W][VEC], bias[VEC], win[W - 1][VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][v] = a.weight[(size_t)(c0 + v) * W + j];
-        bias[v] = a.bias ? a.bias[c0 + v] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) unpack(before[i], win[i]);
+    int left = min(t0 + run, len) - t0;
+    if (left <= 0) return;
 
     x += t0 * a.xs.t;
     T *y = (T *)a.y + (((size_t)b * a.H + head) * a.T + t0) * a.d + j0;
-    for (int t = t0; t < t1; t += U) {
-        V in[U];
+    V now[U], next[U];
+    auto fetch = [&](V *rows, int n) {   // the next U rows, of which n exist
 #pragma unroll
-        for (int u = 0; u < U; ++u) in[u] = t + u < t1 ? *(const V *)(x + u * a.xs.t) : zero_pack<V>();
+        for (int u = 0; u < U; ++u) {
+            rows[u] = load_if((const V *)x, u < n);
+            x += a.xs.t;
+        }
+    };
+    fetch(now, left);
+    float w[W][VEC], bias[VEC], win[W - 1][VEC];
+    load_taps<VEC, W>(a.weight, a.bias, c0, w, bias);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) unpack(before[i], win[i]);
+    for (; left > 0; left -= U) {
+        fetch(next, left - U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float cur[VEC], acc[VEC];
-            unpack(in[u], cur);
+            unpack(now[u], cur);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 float s = bias[v];
@@ -124,50 +153,64 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
                 for (int i = 0; i + 1 < W - 1; ++i) win[i][v] = win[i + 1][v];
                 win[W - 2][v] = cur[v];
             }
-            if (t + u < t1) {
+            if (u < left) {
                 V out;
                 pack(out, acc);
-                *(V *)(y + (size_t)u * a.d) = out;
+                *(V *)y = out;
             }
+            y += a.d;
+            now[u] = next[u];
         }
-        x += U * a.xs.t;
-        y += (size_t)U * a.d;
     }
 }
 
-// One token per row: x [B, D] (row stride xs.b), state [B, W-1, D] shifted in place.
+// One token per row: x [B, D] (row stride xs.b), state [B, W-1, D] shifted in
+// place.  A thread takes ROWS batch rows, so the taps are read once for them
+// and all of its rows' loads are in flight together.
+constexpr int kStepRows = 4;
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a)
 {
     using V = typename Pack<T, VEC>::V;
     const int D = a.d;
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    const int b = blockIdx.x * blockDim.y + threadIdx.y;
-    if (c0 >= D || b >= a.B) return;
-    T *st = (T *)a.state_out + (size_t)b * (W - 1) * D + c0;
-    V rows[W];
+    const int b0 = (blockIdx.x * blockDim.y + threadIdx.y) * kStepRows;
+    if (c0 >= D) return;
+    V rows[kStepRows][W];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) rows[i] = *(const V *)(st + (size_t)i * D);
-    rows[W - 1] = *(const V *)((const T *)a.x + b * a.xs.b + c0);
-    float acc[VEC];
+    for (int r = 0; r < kStepRows; ++r) {
+        if (b0 + r >= a.B) break;
+        const T *st = (const T *)a.state_out + (size_t)(b0 + r) * (W - 1) * D + c0;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) acc[v] = a.bias ? a.bias[c0 + v] : 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        float f[VEC];
-        unpack(rows[i], f);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) acc[v] = fmaf(a.weight[(size_t)(c0 + v) * W + i], f[v], acc[v]);
+        for (int i = 0; i < W - 1; ++i) rows[r][i] = *(const V *)(st + (size_t)i * D);
+        rows[r][W - 1] = *(const V *)((const T *)a.x + (b0 + r) * a.xs.b + c0);
     }
-    if (a.silu) {
+    float w[W][VEC], bias[VEC];
+    load_taps<VEC, W>(a.weight, a.bias, c0, w, bias);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) acc[v] *= sigmoid_f32(acc[v]);
+    for (int r = 0; r < kStepRows; ++r) {
+        if (b0 + r >= a.B) break;
+        float acc[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[v] = bias[v];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float f[VEC];
+            unpack(rows[r][i], f);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) acc[v] = fmaf(w[i][v], f[v], acc[v]);
+        }
+        if (a.silu) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) acc[v] *= sigmoid_f32(acc[v]);
+        }
+        V out;
+        pack(out, acc);
+        *(V *)((T *)a.y + (size_t)(b0 + r) * D + c0) = out;
+        T *st = (T *)a.state_out + (size_t)(b0 + r) * (W - 1) * D + c0;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) *(V *)(st + (size_t)i * D) = rows[r][i + 1];
     }
-    V out;
-    pack(out, acc);
-    *(V *)((T *)a.y + (size_t)b * D + c0) = out;
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) *(V *)(st + (size_t)i * D) = rows[i + 1];
 }
 
 // ------------------------------------------------------------- backward
@@ -184,10 +227,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a)
 // partial sums are added by a second kernel in a fixed order, so the result
 // does not depend on scheduling.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvBwdArgs a, int run, int runs, float *part)
+__global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int run, int runs, float *part)
 {
     using V = typename Pack<T, VEC>::V;
-    constexpr int U = VEC > 1 ? 4 : 8;
+    constexpr int U = VEC == 1 ? 8 : sizeof(T) == 4 ? 2 : 4;   // as in the forward
     const int D = a.H * a.d;
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
     const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -208,15 +251,11 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvBwdArgs a, i
         T *dst = a.dstate ? (T *)a.dstate + (size_t)b * (W - 1) * D + c0 : nullptr;
 
         float w[W][VEC], bias[VEC], win[W - 1][VEC], dp[W][VEC];
+        load_taps<VEC, W>(a.weight, a.bias, c0, w, bias);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
+        for (int v = 0; v < VEC; ++v)
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                w[j][v] = a.weight[(size_t)(c0 + v) * W + j];
-                dp[j][v] = 0.f;
-            }
-            bias[v] = a.bias ? a.bias[c0 + v] : 0.f;
-        }
+            for (int j = 0; j < W; ++j) dp[j][v] = 0.f;
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             const int r = t0 - (W - 1) + i;
@@ -225,20 +264,26 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvBwdArgs a, i
             unpack(v, win[i]);
         }
         // rows the walk completes: [-(W-1), t1) from a row's first run, [t0, t1) from the others
-        const int tend = t1 + (W - 1);
-        for (int t = t0; t < tend; t += U) {
-            V xin[U], gin[U];
+        const int tend = t1 + (W - 1), live_end = min(len, tend), rmin = first ? -(W - 1) : t0;
+        const T *xr = x + t0 * a.xs.t, *gr = dy + t0 * a.dys.t;
+        V xin[U], gin[U], xnext[U], gnext[U];
+        auto fetch = [&](V *xs, V *gs, int t) {   // U rows from t on
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool live = t + u < len && t + u < tend;
-                xin[u] = live ? *(const V *)(x + (t + u) * a.xs.t) : zero_pack<V>();
-                gin[u] = live ? *(const V *)(dy + (t + u) * a.dys.t) : zero_pack<V>();
+                const bool live = t + u < live_end;
+                xs[u] = load_if((const V *)xr, live);
+                gs[u] = load_if((const V *)gr, live);
+                xr += a.xs.t;
+                gr += a.dys.t;
             }
+        };
+        // U tokens; `inside`: all of them are the run's and live, and so are the rows they complete
+        auto walk = [&](int t, auto inside) {
+            constexpr bool FULL = decltype(inside)::value;
+            T *dxr = dx + (t - (W - 1)) * a.dxs.t;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int tt = t + u;
-                if (tt >= tend) break;
-                const bool mine = tt < t1;
                 float cur[VEC], g[VEC], out[VEC];
                 unpack(xin[u], cur);
                 unpack(gin[u], g);
@@ -253,38 +298,49 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvBwdArgs a, i
                         const float q = sigmoid_f32(s);
                         p *= fmaf(s * q, 1.f - q, q);
                     }
-                    if (tt >= len) p = 0.f;
+                    if (!FULL && tt >= live_end) p = 0.f;
 #pragma unroll
                     for (int i = 0; i < W - 1; ++i) dp[i][v] = dp[i + 1][v];
                     dp[W - 1][v] = p;
-                    if (mine) {
+                    if (FULL || tt < t1) {
 #pragma unroll
                         for (int i = 0; i < W - 1; ++i) dw[i][v] = fmaf(p, win[i][v], dw[i][v]);
                         dw[W - 1][v] = fmaf(p, cur[v], dw[W - 1][v]);
                         db[v] += p;
                     }
-                    float acc = 0.f;
+                    float acc = w[0][v] * dp[W - 1][v];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) acc = fmaf(w[j][v], dp[W - 1 - j][v], acc);
+                    for (int j = 1; j < W; ++j) acc = fmaf(w[j][v], dp[W - 1 - j][v], acc);
                     out[v] = acc;
 #pragma unroll
                     for (int i = 0; i + 1 < W - 1; ++i) win[i][v] = win[i + 1][v];
                     win[W - 2][v] = cur[v];
                 }
                 const int r = tt - (W - 1);
-                if (r < t0 && !first) continue;
-                if (dso && r >= len - (W - 1) && r < len) {
-                    float f[VEC];
-                    unpack(*(const V *)(dso + (size_t)(r - len + W - 1) * D), f);
+                if (FULL || (r >= rmin && r < t1)) {
+                    if (!FULL && dso && r >= len - (W - 1) && r < len) {
+                        float f[VEC];
+                        unpack(*(const V *)(dso + (size_t)(r - len + W - 1) * D), f);
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) out[v] += f[v];
+                        for (int v = 0; v < VEC; ++v) out[v] += f[v];
+                    }
+                    V o;
+                    pack(o, out);
+                    if (FULL || r >= 0) *(V *)dxr = o;
+                    else if (dst) *(V *)(dst + (size_t)(r + W - 1) * D) = o;
                 }
-                V o;
-                pack(o, out);
-                if (r >= 0)
-                    *(V *)(dx + r * a.dxs.t) = o;
-                else if (dst)
-                    *(V *)(dst + (size_t)(r + W - 1) * D) = o;
+                dxr += a.dxs.t;
+            }
+        };
+        fetch(xin, gin, t0);
+        for (int t = t0; t < tend; t += U) {
+            fetch(xnext, gnext, t + U);
+            if (t >= t0 + W - 1 && t + U <= t1 && t + U <= len) walk(t, std::true_type{});
+            else walk(t, std::false_type{});
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                xin[u] = xnext[u];
+                gin[u] = gnext[u];
             }
         }
     }
@@ -345,7 +401,7 @@ template <typename T> bool conv_vectors(int d, int vec, const void *const *ptrs,
 template <typename T, int VEC, int W>
 cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
 {
-    const ConvGrid g = conv_grid(a.B, a.T, (long long)a.H * a.d / VEC, 512, 64);
+    const ConvGrid g = conv_grid(a.B, a.T, (long long)a.H * a.d / VEC, kConvThreads, 768, 256);
     conv_fwd_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a, g.run, g.runs);
     return cudaGetLastError();
 }
@@ -353,13 +409,13 @@ cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
 template <typename T, int VEC, int W>
 cudaError_t conv_step(const ConvArgs &a, cudaStream_t st)
 {
-    const ConvGrid g = conv_grid(a.B, 1, a.d / VEC, 512, 8);
+    const ConvGrid g = conv_grid((a.B + kStepRows - 1) / kStepRows, 1, a.d / VEC, kConvThreads, 512, 8);
     conv_step_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a);
     return cudaGetLastError();
 }
 
-constexpr int kBwdLongest = 128;
-ConvGrid conv_bwd_grid(int B, int T, long long vectors) { return conv_grid(B, T, vectors, 512, kBwdLongest); }
+// Four runs a block, so that a block's partial sums of dweight are few.
+ConvGrid conv_bwd_grid(int B, int T, long long vectors) { return conv_grid(B, T, vectors, 32, 512, 256); }
 
 template <typename T, int VEC, int W>
 cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
@@ -376,13 +432,20 @@ cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
 
 enum Form { FWD, STEP };
 
+template <typename T, int VEC, int W, Form F>
+cudaError_t conv_form(const ConvArgs &a, cudaStream_t st)
+{
+    if constexpr (F == FWD) return conv_fwd<T, VEC, W>(a, st);
+    else return conv_step<T, VEC, W>(a, st);
+}
+
 template <typename T, int VEC, Form F>
 cudaError_t by_width(const ConvArgs &a, cudaStream_t st)
 {
     switch (a.W) {
-        case 2: return F == FWD ? conv_fwd<T, VEC, 2>(a, st) : conv_step<T, VEC, 2>(a, st);
-        case 3: return F == FWD ? conv_fwd<T, VEC, 3>(a, st) : conv_step<T, VEC, 3>(a, st);
-        default: return F == FWD ? conv_fwd<T, VEC, 4>(a, st) : conv_step<T, VEC, 4>(a, st);
+        case 2: return conv_form<T, VEC, 2, F>(a, st);
+        case 3: return conv_form<T, VEC, 3, F>(a, st);
+        default: return conv_form<T, VEC, 4, F>(a, st);
     }
 }
 
@@ -391,8 +454,8 @@ cudaError_t by_type(const ConvArgs &a, cudaStream_t st)
 {
     const void *p[] = {a.x, a.state, a.y, a.state_out};
     if (a.bf16)
-        return conv_vectors<__nv_bfloat16>(a.d, 8, p, 4, &a.xs, 1) ? by_width<__nv_bfloat16, 8, F>(a, st)
-                                                                   : by_width<__nv_bfloat16, 1, F>(a, st);
+        return conv_vectors<__nv_bfloat16>(a.d, F == FWD ? 4 : 8, p, 4, &a.xs, 1)
+                   ? by_width<__nv_bfloat16, F == FWD ? 4 : 8, F>(a, st) : by_width<__nv_bfloat16, 1, F>(a, st);
     return conv_vectors<float>(a.d, 4, p, 4, &a.xs, 1) ? by_width<float, 4, F>(a, st) : by_width<float, 1, F>(a, st);
 }
 

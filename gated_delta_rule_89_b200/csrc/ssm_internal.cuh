@@ -143,11 +143,12 @@ __device__ __forceinline__ f32x2 exp2_approx2(f32x2 x)
 {
     return make_f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
 }
-// The decays 2^(delta A2) of two states.  The hardware's 2^x lies below the
+// The decay 2^(delta A2) of a state, and of two.  The hardware's 2^x lies below the
 // exact value by 2e-8 at the mean where it is close to 1, and a slowly
 // decaying state multiplies a thousand of them; raising the exponent by 2e-8
 // leaves a mean error under 1e-8 between 2^-16 and 2^-1 (measured), at no
 // cost, and 2^(2e-8) is still exactly 1, so a time step of 0 keeps the state.
+__device__ __forceinline__ float decay(float delta, float A2) { return exp2_approx(fmaf(delta, A2, 2e-8f)); }
 __device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
 {
     return exp2_approx2(fma2(delta, A2, both(2e-8f)));
@@ -180,6 +181,32 @@ __device__ __forceinline__ float softplus_f32(float x, float &e)
 {
     e = exp2_approx(-kLog2e * fabsf(x));
     return fmaxf(x, 0.f) + log1p_unit(e);
+}
+
+// Sums v[0..COUNT) over the lanes that differ in the bits from MASK up to
+// END / 2.  Each step a lane hands half of its values to its partner and keeps
+// the other half, so COUNT / (lanes) values stay with every lane (one,
+// replicated, when the lanes outnumber the values); `which` is the first index
+// it kept.
+template <int COUNT, int MASK, int END>
+__device__ __forceinline__ void lane_sums(float *v, int lane, int &which)
+{
+    if constexpr (MASK < END) {
+        if constexpr (COUNT > 1) {
+            constexpr int H = COUNT / 2;
+            const bool up = lane & MASK;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float send = up ? v[i] : v[i + H], keep = up ? v[i + H] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, MASK);
+            }
+            if (up) which += H;
+            lane_sums<H, MASK * 2, END>(v, lane, which);
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], MASK);
+            lane_sums<1, MASK * 2, END>(v, lane, which);
+        }
+    }
 }
 
 // N consecutive elements from / to memory as fp32.  VECTOR: one access of
@@ -237,23 +264,64 @@ __device__ __forceinline__ int row_length(const int *lengths, int b, int T)
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
+// A read-only load that a predicate can leave out (then 0), without a branch:
+// a thread's loads stay together instead of waiting for one another.
+__device__ __forceinline__ float4 load_if(const float4 *p, bool on)
+{
+    float4 v;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+        "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w) : "l"(p), "r"((int)on));
+    return v;
+}
+__device__ __forceinline__ uint4 load_if(const uint4 *p, bool on)
+{
+    uint4 v;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+        "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)on));
+    return v;
+}
+__device__ __forceinline__ uint2 load_if(const uint2 *p, bool on)
+{
+    uint2 v;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y) : "l"(p), "r"((int)on));
+    return v;
+}
+__device__ __forceinline__ float load_if(const float *p, bool on)
+{
+    float v;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
+        : "=&f"(v) : "l"(p), "r"((int)on));
+    return v;
+}
+__device__ __forceinline__ unsigned short load_if(const unsigned short *p, bool on)
+{
+    unsigned short v;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+        : "=&h"(v) : "l"(p), "r"((int)on));
+    return v;
+}
+
 // 4 consecutive elements, of which the first `valid` exist (the rest are 0).
 // VECTOR: groups are whole and aligned, so valid is <= 0 or >= 4.
 template <typename T, bool VECTOR>
 __device__ __forceinline__ typename Pack<T, 4>::V load4(const T *p, int valid)
 {
     using V = typename Pack<T, 4>::V;
-    V v = zero_pack<V>();
-    if (VECTOR) {
-        if (valid > 0) v = __ldg((const V *)p);
+    if constexpr (VECTOR) {
+        return load_if((const V *)p, valid > 0);
     } else {
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        using E = typename Pack<T, 1>::V;
+        float f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < valid) f[k] = to_f32<T>(__ldg(p + k));
+        for (int k = 0; k < 4; ++k) unpack(load_if((const E *)p + k, k < valid), f + k);
+        V v;
         pack(v, f);
+        return v;
     }
-    return v;
 }
 template <typename T, bool VECTOR>
 __device__ __forceinline__ void store4(T *p, const float *f, int valid)

@@ -375,51 +375,71 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 // ------------------------------------------------------------ single token
 //
 // The state is read once and written once (8 N bytes a channel) and bounds
-// the step; a thread owns 4 states, so a warp's accesses are whole lines.
-template <typename T, int N>
+// the step.  A thread owns 4 states of a channel in ROWS batch rows, so a
+// warp's accesses are whole lines, several loads are in flight, and A is read
+// once for the rows; each of a channel's lanes forms the time step and the
+// output of one row.
+template <typename T, int N, bool VECTOR>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const ScanArgs a, int blocks_per_row)
 {
-    constexpr int LPC = N / 4, CB = 256 / LPC;
-    const int b = blockIdx.x / blocks_per_row;
-    const int c = (blockIdx.x - b * blocks_per_row) * CB + threadIdx.x / LPC;
-    const int n0 = (threadIdx.x % LPC) * 4;
+    constexpr int LPC = N / 4, CB = 256 / LPC, ROWS = LPC < 4 ? LPC : 4;
+    const int group = blockIdx.x / blocks_per_row, b0 = group * ROWS;
+    const int c = (blockIdx.x - group * blocks_per_row) * CB + threadIdx.x / LPC;
+    const int ln = threadIdx.x % LPC, n0 = ln * 4;
     const bool on = c < a.D;
-    float y = 0.f;
-    if (on) {
-        float4 *ph = (float4 *)(a.h_T + ((size_t)b * a.D + c) * N + n0);
-        const float4 h = __ldcs(ph);
-        const float4 A = *(const float4 *)(a.A + (size_t)c * N + n0);
-        const float x = to_f32<T>(((const T *)a.x)[b * a.xs.b + c]);
-        float d = to_f32<T>(((const T *)a.dt)[b * a.dts.b + c]);
-        const int g = c / (a.D / a.G);
-        const T *pB = (const T *)a.Bm + b * a.bs.b + (size_t)g * N + n0;
-        const T *pC = (const T *)a.Cm + b * a.cs.b + (size_t)g * N + n0;
-        if (a.dt_bias) d += a.dt_bias[c];
-        if (a.softplus) {
-            float e;
-            d = softplus_f32(d, e);
-        }
-        const float u = d * x, d2 = d * kLog2e;
-        float4 r;
-        r.x = fmaf(exp2_approx(d2 * A.x), h.x, u * to_f32<T>(pB[0]));
-        r.y = fmaf(exp2_approx(d2 * A.y), h.y, u * to_f32<T>(pB[1]));
-        r.z = fmaf(exp2_approx(d2 * A.z), h.z, u * to_f32<T>(pB[2]));
-        r.w = fmaf(exp2_approx(d2 * A.w), h.w, u * to_f32<T>(pB[3]));
-        __stcs(ph, r);
-        y = to_f32<T>(pC[0]) * r.x;
-        y = fmaf(to_f32<T>(pC[1]), r.y, y);
-        y = fmaf(to_f32<T>(pC[2]), r.z, y);
-        y = fmaf(to_f32<T>(pC[3]), r.w, y);
-        if (n0 == 0 && a.D_skip) y = fmaf(a.D_skip[c], x, y);
-    }
+    float4 *ph = (float4 *)(a.h_T + ((size_t)b0 * a.D + c) * N + n0);
+    const size_t hrow = (size_t)a.D * N / 4;
+    float4 h[ROWS];
 #pragma unroll
-    for (int o = LPC / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (on && n0 == 0) {
-        if (a.z) {
-            const float z = to_f32<T>(((const T *)a.z)[b * a.zs.b + c]);
-            y *= z * sigmoid_f32(z);
+    for (int r = 0; r < ROWS; ++r)
+        h[r] = on && b0 + r < a.B ? __ldcs(ph + r * hrow) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // the row whose sum lane_sums leaves with this lane
+    const int mine = ROWS == 4 ? (ln & 1) * 2 + (ln >> 1 & 1) : ln & 1;
+    const int bm = b0 + mine;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    float x = 0.f, d = 0.f, z = 0.f;
+    if (on) {
+        A = *(const float4 *)(a.A + (size_t)c * N + n0);
+        if (bm < a.B) {
+            x = to_f32<T>(((const T *)a.x)[bm * a.xs.b + c]);
+            d = to_f32<T>(((const T *)a.dt)[bm * a.dts.b + c]);
+            if (a.z) z = to_f32<T>(((const T *)a.z)[bm * a.zs.b + c]);
+            if (a.dt_bias) d += a.dt_bias[c];
+            if (a.softplus) {
+                float e;
+                d = softplus_f32(d, e);
+            }
         }
-        ((T *)a.y)[(size_t)b * a.D + c] = from_f32<T>(y);
+    }
+    const int g = on ? c / (a.D / a.G) : 0;
+    const T *pB = (const T *)a.Bm + (size_t)g * N + n0, *pC = (const T *)a.Cm + (size_t)g * N + n0;
+    const float u = d * x, d2 = d * kLog2e;
+    float y[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int from = ROWS == 4 ? (r >> 1) + (r & 1) * 2 : r;      // the lane whose row r is
+        const float dr = __shfl_sync(0xffffffffu, d2, from, LPC), ur = __shfl_sync(0xffffffffu, u, from, LPC);
+        y[r] = 0.f;
+        if (on && b0 + r < a.B) {
+            float fb[4], fc[4];
+            unpack(load4<T, VECTOR>(pB + (b0 + r) * a.bs.b, 4), fb);
+            unpack(load4<T, VECTOR>(pC + (b0 + r) * a.cs.b, 4), fc);
+            float4 &s = h[r];
+            s.x = fmaf(decay(dr, A.x), s.x, ur * fb[0]);
+            s.y = fmaf(decay(dr, A.y), s.y, ur * fb[1]);
+            s.z = fmaf(decay(dr, A.z), s.z, ur * fb[2]);
+            s.w = fmaf(decay(dr, A.w), s.w, ur * fb[3]);
+            __stcs(ph + r * hrow, s);
+            y[r] = fmaf(fc[3], s.w, fmaf(fc[2], s.z, fmaf(fc[1], s.y, fc[0] * s.x)));
+        }
+    }
+    int which = 0;
+    lane_sums<ROWS, 1, LPC>(y, ln, which);
+    if (on && ln < ROWS && bm < a.B) {
+        float out = y[0];
+        if (a.D_skip) out = fmaf(a.D_skip[c], x, out);
+        if (a.z) out *= z * sigmoid_f32(z);
+        ((T *)a.y)[(size_t)bm * a.D + c] = from_f32<T>(out);
     }
 }
 
@@ -537,8 +557,13 @@ cudaError_t scan_by_layout(const ScanArgs &a, const Extra &x, cudaStream_t st, i
 template <typename T, int N>
 cudaError_t step_typed(const ScanArgs &a, cudaStream_t st)
 {
-    const int cb = 1024 / N, bpr = (a.D + cb - 1) / cb;
-    ssm_step_kernel<T, N><<<(unsigned)((long long)a.B * bpr), 256, 0, st>>>(a, bpr);
+    const int cb = 1024 / N, bpr = (a.D + cb - 1) / cb, rows = N / 4 < 4 ? N / 4 : 4;
+    const unsigned blocks = (unsigned)((long long)((a.B + rows - 1) / rows) * bpr);
+    const size_t quad = 4 * sizeof(T);
+    if (aligned_to(a.Bm, quad) && aligned_to(a.Cm, quad) && a.bs.b % 4 == 0 && a.cs.b % 4 == 0)
+        ssm_step_kernel<T, N, true><<<blocks, 256, 0, st>>>(a, bpr);
+    else
+        ssm_step_kernel<T, N, false><<<blocks, 256, 0, st>>>(a, bpr);
     return cudaGetLastError();
 }
 

@@ -81,31 +81,6 @@ struct BwdParts {
     BackPieces pc;
 };
 
-// Sums v[0..COUNT) over the lanes that differ in the bits from MASK up to 16.
-// Each step a lane hands half of its values to its partner and keeps the other
-// half, so COUNT / CL values stay with every lane (one, replicated, when the
-// lanes outnumber the values); `which` is the first index it kept.
-template <int COUNT, int MASK>
-__device__ __forceinline__ void lane_sums(float *v, int lane, int &which)
-{
-    if constexpr (MASK < 32) {
-        if constexpr (COUNT > 1) {
-            constexpr int H = COUNT / 2;
-            const bool up = lane & MASK;
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const float send = up ? v[i] : v[i + H], keep = up ? v[i + H] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, MASK);
-            }
-            if (up) which += H;
-            lane_sums<H, MASK * 2>(v, lane, which);
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], MASK);
-            lane_sums<1, MASK * 2>(v, lane, which);
-        }
-    }
-}
-
 template <typename T, int N, bool VECTOR>
 __global__ void __launch_bounds__(kThreads, 1)
 ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
@@ -209,7 +184,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                 };
                 auto store = [&](Sums &k, int t) {
                     int which = 0;
-                    lane_sums<8, S::LN>(k.v, lane, which);
+                    lane_sums<8, S::LN, 32>(k.v, lane, which);
                     *(float2 *)(o2 + t * kLanes * 2) = make_float2(k.su, k.sw);
                     if (f.z) o1[t * kLanes] = k.sy;
                     constexpr int left = 8 / S::CL > 1 ? 8 / S::CL : 1;

@@ -19,78 +19,111 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _DTYPES, _check, _need, _to_device, _to_host, lib
+from . import _DTYPES, _check, _to_device, _to_host, lib
 
 _ACTIVATIONS = {None: 0, "silu": 1}
+_F32, _I32 = torch.float32, torch.int32
 _I64x3 = ctypes.c_longlong * 3
 _I64x5 = ctypes.c_longlong * 5
 _I64x10 = ctypes.c_longlong * 10
 _I64x12 = ctypes.c_longlong * 12
+# A decode step takes a few microseconds on the device, so the host's share counts: these two are
+# what torch.cuda.current_device() and current_stream() come to, without the objects around them.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _scoped(dev: torch.device, stream, body):
-    """body(stream handle) with the device and the stream current that the call runs on."""
+def _run(call, x, stream, *args):
+    """call(stream handle, device index, x, *args) with the device and the stream current that it
+    runs on, so that what it allocates belongs to that stream.  A host x: every tensor is copied
+    to the current device first and the results back afterwards."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    if x.is_cuda:
+        index = x.get_device()
+        if stream is None and index == _current_device():
+            return call(_current_stream(index), index, x, *args)
+        host = False
+    else:
+        _type_of(x)
+        index, host = torch.cuda.current_device(), True
+    dev = torch.device("cuda", index)
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return body(torch.cuda.current_stream().cuda_stream)
         with torch.cuda.device(dev):
-            return body(torch.cuda.current_stream().cuda_stream)
-    if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.current_stream()
+    elif not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
-
-
-def _device(x: torch.Tensor) -> torch.device:
-    return x.device if x.is_cuda else torch.device("cuda", torch.cuda.current_device())
+        if host:
+            x = _to_device(x, dev)
+            args = [_to_device(t, dev) if isinstance(t, torch.Tensor) else t for t in args]
+        out = call(stream.cuda_stream, index, x, *args)
+        return tuple(_to_host(t) for t in out) if host else out
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, dev, dense: int = 1):
-    """A tensor of the given shape whose last `dense` dimensions are contiguous."""
+def _refuse(t, name, shape, index, dtype):
+    """Says what is wrong with a tensor that _dense or _rows did not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        step = 1
-        for k in range(1, dense + 1):
-            if t.shape[-k] != 1 and t.stride(-k) != step and t.numel():
-                raise ValueError(f"the last dimension{'s' if dense > 1 else ''} of {name} must be contiguous")
-            step *= t.shape[-k]
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _vector(t: Optional[torch.Tensor], name: str, shape, dev, dtype=torch.float32):
-    if t is not None:
-        _need(t, name, dtype, dev)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _dense(t, name, shape, index, dtype=_F32):
+    """A contiguous tensor of the given shape."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, index, dtype)
 
 
-def _type_of(x: torch.Tensor):
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a tensor")
+def _rows(t, name, shape, index, dtype, dense=1):
+    """A tensor of the given shape whose last `dense` dimensions are contiguous."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape:
+            if t.is_contiguous() or not t.numel():
+                return
+            step, strides = 1, t.stride()
+            for k in range(1, dense + 1):
+                if shape[-k] != 1 and strides[-k] != step:
+                    raise ValueError(f"the last dimension{'s' if dense > 1 else ''} of {name} must be contiguous")
+                step *= shape[-k]
+            return
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, index, dtype)
+
+
+def _type_of(x):
     if x.dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16")
     return x.dtype
 
 
-def _workspace(ws: Optional[torch.Tensor], size: int, dev):
+def _new(shape, dtype, index, zero=False):
+    return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=index)
+
+
+def _workspace(ws, size, index):
     if not size:
         return None
     if ws is None or ws.numel() * ws.element_size() < size:
-        return torch.empty(size, dtype=torch.uint8, device=dev)
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
+        return torch.empty(size, dtype=torch.uint8, device=index)
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index}")
     return ws
 
 
@@ -98,9 +131,10 @@ def _workspace(ws: Optional[torch.Tensor], size: int, dev):
 
 def _conv_shape(x):
     """(B, H, T, d) of [B,H,T,d] or [B,T,D] (one head)."""
-    if x.dim() == 4:
-        return tuple(x.shape)
-    if x.dim() == 3:
+    n = x.dim()
+    if n == 4:
+        return x.shape
+    if n == 3:
         B, T, D = x.shape
         return B, 1, T, D
     raise ValueError("x must be [B,H,T,d] or [B,T,D]")
@@ -111,14 +145,17 @@ def _conv_strides(x):
     return _I64x3(s[0], s[1], s[2]) if len(s) == 4 else _I64x3(s[0], 0, s[1])
 
 
-def _conv_params(weight, bias, activation, D, dev):
+def _conv_params(weight, bias, activation, D, index):
+    """Checks weight and bias; returns (taps, the activation's number)."""
     if activation not in _ACTIVATIONS:
         raise ValueError("activation must be None or 'silu'")
-    _need(weight, "weight", torch.float32, dev)
-    if weight.dim() != 2 or weight.shape[0] != D:
-        raise ValueError(f"weight must be [{D},W], got {list(weight.shape)}")
-    _vector(bias, "bias", (D,), dev)
-    return weight.shape[1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError(f"weight must be a tensor [{D},W]")
+    W = weight.shape[1]
+    _dense(weight, "weight", (D, W), index)
+    if bias is not None:
+        _dense(bias, "bias", (D,), index)
+    return W, _ACTIVATIONS[activation]
 
 
 def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -133,33 +170,33 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     activation "silu" or None; lengths int32 [B].  Returns (y, contiguous in x's shape and
     type, and the state after the prompt or None); ``state_out`` may be ``state``.
     """
+    return _run(_conv_fwd, x, stream, weight, bias, state, activation, lengths, y, state_out, final_state)
+
+
+def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, y, state_out, final_state):
     dt = _type_of(x)
-    dev, host = _device(x), not x.is_cuda
     B, H, T, d = _conv_shape(x)
-    D = H * d
-
-    def body(handle, x=x, weight=weight, bias=bias, state=state, lengths=lengths, y=y, state_out=state_out):
-        if host:
-            x, weight, bias, state, lengths = (_to_device(t, dev) for t in (x, weight, bias, state, lengths))
-        _rows(x, "x", x.shape, dt, dev)
-        W = _conv_params(weight, bias, activation, D, dev)
-        _vector(state, "state", (B, W - 1, D), dev, dt)
-        _vector(lengths, "lengths", (B,), dev, torch.int32)
-        if y is None:
-            y = (torch.empty if lengths is None else torch.zeros)(x.shape, dtype=dt, device=dev)
-        else:
-            _vector(y, "y", x.shape, dev, dt)
-        if state_out is not None:
-            _vector(state_out, "state_out", (B, W - 1, D), dev, dt)
-        elif final_state:
-            state_out = torch.empty(B, max(W - 1, 0), D, dtype=dt, device=dev)
-        _check(lib().gdr_short_conv_fwd(
-            _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths), _ptr(y), _ptr(state_out),
-            _conv_strides(x), B, H, T, d, W, _ACTIVATIONS[activation], _DTYPES[dt], handle), "gdr_short_conv_fwd")
-        return y, state_out
-
-    out = _scoped(dev, stream, body)
-    return tuple(_to_host(t) for t in out) if host else out
+    shape, D = x.shape, H * d
+    _rows(x, "x", shape, index, dt)
+    W, act = _conv_params(weight, bias, activation, D, index)
+    if state is not None:
+        _dense(state, "state", (B, W - 1, D), index, dt)
+    if lengths is not None:
+        _dense(lengths, "lengths", (B,), index, _I32)
+    if y is None:
+        y = _new(shape, dt, index, lengths is not None)
+    else:
+        _dense(y, "y", shape, index, dt)
+    if state_out is not None:
+        _dense(state_out, "state_out", (B, W - 1, D), index, dt)
+    elif final_state:
+        state_out = _new((B, max(W - 1, 0), D), dt, index)
+    status = lib().gdr_short_conv_fwd(
+        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths), y.data_ptr(), _ptr(state_out),
+        _conv_strides(x), B, H, T, d, W, act, _DTYPES[dt], handle)
+    if status:
+        _check(status, "gdr_short_conv_fwd")
+    return y, state_out
 
 
 def short_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -170,27 +207,29 @@ def short_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, 
     x [B,D] (rows may be strided); state [B,W-1,D] in x's type is shifted IN PLACE; weight, bias
     and activation as ``short_conv_fwd``.  Returns y [B,D].
     """
-    dt = _type_of(x)
-    dev = x.device
-    if not x.is_cuda:
+    if isinstance(x, torch.Tensor) and not x.is_cuda:
         raise ValueError("short_conv_step works on CUDA tensors: the state is updated in place")
+    return _run(_conv_step, x, stream, state, weight, bias, activation, y)
+
+
+def _conv_step(handle, index, x, state, weight, bias, activation, y):
+    dt = _type_of(x)
     if x.dim() != 2:
         raise ValueError("x must be [B,D]")
-    B, D = x.shape
-    _rows(x, "x", x.shape, dt, dev)
-    W = _conv_params(weight, bias, activation, D, dev)
-    _vector(state, "state", (B, W - 1, D), dev, dt)
-
-    def body(handle, y=y):
-        if y is None:
-            y = torch.empty(B, D, dtype=dt, device=dev)
-        else:
-            _vector(y, "y", (B, D), dev, dt)
-        _check(lib().gdr_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), x.stride(0), B, D,
-                                         W, _ACTIVATIONS[activation], _DTYPES[dt], handle), "gdr_short_conv_step")
-        return y
-
-    return _scoped(dev, stream, body)
+    shape = x.shape
+    B, D = shape
+    _rows(x, "x", shape, index, dt)
+    W, act = _conv_params(weight, bias, activation, D, index)
+    _dense(state, "state", (B, W - 1, D), index, dt)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=index)
+    else:
+        _dense(y, "y", shape, index, dt)
+    status = lib().gdr_short_conv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), y.data_ptr(),
+                                       x.stride()[0], B, D, W, act, _DTYPES[dt], handle)
+    if status:
+        _check(status, "gdr_short_conv_step")
+    return y
 
 
 def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -205,70 +244,64 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias
     state).  dx has x's shape and its order in memory (token rows stay token rows); it is
     zero behind a row's end.
     """
+    return _run(_conv_bwd, x, stream, weight, dy, bias, state, dstate_out, activation, lengths, workspace)
+
+
+def _conv_bwd(handle, index, x, weight, dy, bias, state, dstate_out, activation, lengths, workspace):
     dt = _type_of(x)
-    dev, host = _device(x), not x.is_cuda
     B, H, T, d = _conv_shape(x)
-    D = H * d
-
-    def body(handle, x=x, weight=weight, dy=dy, bias=bias, state=state, dstate_out=dstate_out, lengths=lengths):
-        if host:
-            x, weight, dy, bias, state, dstate_out, lengths = (
-                _to_device(t, dev) for t in (x, weight, dy, bias, state, dstate_out, lengths))
-        _rows(x, "x", x.shape, dt, dev)
-        _rows(dy, "dy", x.shape, dt, dev)
-        W = _conv_params(weight, bias, activation, D, dev)
-        _vector(state, "state", (B, W - 1, D), dev, dt)
-        _vector(dstate_out, "dstate_out", (B, W - 1, D), dev, dt)
-        _vector(lengths, "lengths", (B,), dev, torch.int32)
-        if x.dim() == 4 and x.stride(1) < x.stride(2):
-            dx = torch.empty(B, T, H, d, dtype=dt, device=dev).transpose(1, 2)
-        else:
-            dx = torch.empty(x.shape, dtype=dt, device=dev)
-        dweight = torch.empty(D, W, dtype=torch.float32, device=dev)
-        dbias = None if bias is None else torch.empty(D, dtype=torch.float32, device=dev)
-        dstate = None if state is None else torch.empty(B, W - 1, D, dtype=dt, device=dev)
-        L = lib()
-        size = L.gdr_short_conv_bwd_workspace_size(B, H, T, d, W, _DTYPES[dt])
-        ws = _workspace(workspace, size, dev)
-        _check(L.gdr_short_conv_bwd(
-            _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(lengths), _ptr(dy), _ptr(dstate_out), _ptr(dx),
-            _ptr(dweight), _ptr(dbias), _ptr(dstate), _conv_strides(x), _conv_strides(dy), _conv_strides(dx),
-            B, H, T, d, W, _ACTIVATIONS[activation], _DTYPES[dt], _ptr(ws), size, handle), "gdr_short_conv_bwd")
-        return dx, dweight, dbias, dstate
-
-    out = _scoped(dev, stream, body)
-    return tuple(_to_host(t) for t in out) if host else out
+    shape, D = x.shape, H * d
+    _rows(x, "x", shape, index, dt)
+    _rows(dy, "dy", shape, index, dt)
+    W, act = _conv_params(weight, bias, activation, D, index)
+    if state is not None:
+        _dense(state, "state", (B, W - 1, D), index, dt)
+    if dstate_out is not None:
+        _dense(dstate_out, "dstate_out", (B, W - 1, D), index, dt)
+    if lengths is not None:
+        _dense(lengths, "lengths", (B,), index, _I32)
+    if len(shape) == 4 and x.stride(1) < x.stride(2):
+        dx = _new((B, T, H, d), dt, index).transpose(1, 2)
+    else:
+        dx = _new(shape, dt, index)
+    dweight = _new((D, W), _F32, index)
+    dbias = None if bias is None else _new((D,), _F32, index)
+    dstate = None if state is None else _new((B, W - 1, D), dt, index)
+    L = lib()
+    size = L.gdr_short_conv_bwd_workspace_size(B, H, T, d, W, _DTYPES[dt])
+    ws = _workspace(workspace, size, index)
+    status = L.gdr_short_conv_bwd(
+        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths), dy.data_ptr(), _ptr(dstate_out),
+        dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(dstate), _conv_strides(x), _conv_strides(dy),
+        _conv_strides(dx), B, H, T, d, W, act, _DTYPES[dt], _ptr(ws), size, handle)
+    if status:
+        _check(status, "gdr_short_conv_bwd")
+    return dx, dweight, dbias, dstate
 
 
 # ------------------------------------------------------------ state space scan
 
-def _scan_inputs(x, dt_, A, Bm, Cm, D_skip, z, dt_bias, lead, dev):
+def _scan_inputs(index, x, dt, A, Bm, Cm, D_skip, z, dt_bias):
     """Checks what the three scan calls share; returns (G, N)."""
-    dt, D = x.dtype, x.shape[-1]
-    _rows(x, "x", x.shape, dt, dev)
-    _rows(dt_, "dt", x.shape, dt, dev)
+    ty, shape = _type_of(x), x.shape
+    _rows(x, "x", shape, index, ty)
+    _rows(dt, "dt", shape, index, ty)
     if z is not None:
-        _rows(z, "z", x.shape, dt, dev)
-    if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
-        raise ValueError(f"Bm and Cm must be [{'B,T' if len(lead) == 2 else 'B'},G,N]")
-    G, N = Bm.shape[-2:]
-    _rows(Bm, "Bm", lead + (G, N), dt, dev, 2)
-    _rows(Cm, "Cm", lead + (G, N), dt, dev, 2)
-    if G < 1 or D % G:
-        raise ValueError(f"{G} groups do not divide {D} channels")
-    _vector(A, "A", (D, N), dev)
-    if A is None:
-        raise TypeError("A must be a tensor")
-    _vector(D_skip, "D_skip", (D,), dev)
-    _vector(dt_bias, "dt_bias", (D,), dev)
+        _rows(z, "z", shape, index, ty)
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(shape) + 1:
+        raise ValueError(f"Bm and Cm must be [{'B,T' if len(shape) == 3 else 'B'},G,N]")
+    lead = Bm.shape
+    G, N, D = lead[-2], lead[-1], shape[-1]
+    if lead[:-2] != shape[:-1] or G < 1 or D % G:
+        raise ValueError(f"Bm {list(lead)} does not fit x {list(shape)}: [..., G, N] with G dividing {D}")
+    _rows(Bm, "Bm", lead, index, ty, 2)
+    _rows(Cm, "Cm", lead, index, ty, 2)
+    _dense(A, "A", (D, N), index)
+    if D_skip is not None:
+        _dense(D_skip, "D_skip", (D,), index)
+    if dt_bias is not None:
+        _dense(dt_bias, "dt_bias", (D,), index)
     return G, N
-
-
-def _scan_strides(*tensors):
-    out = []
-    for t in tensors:
-        out += (0, 0) if t is None else t.stride()[:2]
-    return out
 
 
 def ssm_scan_fwd_workspace_size(B, T, D, G=1, N=16, dtype=torch.bfloat16) -> int:
@@ -288,39 +321,41 @@ def ssm_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     A [D,N], D_skip [D], dt_bias [D], h0 [B,D,N] fp32; N in 8, 16, 32, 64; lengths int32 [B].
     Returns (y [B,T,D] in x's type, h_T [B,D,N] fp32 or None); ``h_T`` may be ``h0``.
     """
-    ty = _type_of(x)
-    dev, host = _device(x), not x.is_cuda
+    return _run(_scan_fwd, x, stream, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T,
+                final_state, workspace)
+
+
+def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T, final_state,
+              workspace):
     if x.dim() != 3:
         raise ValueError("x must be [B,T,D]")
-    B, T, D = x.shape
-
-    def body(handle, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D_skip=D_skip, z=z, dt_bias=dt_bias, h0=h0, lengths=lengths, y=y,
-             h_T=h_T):
-        if host:
-            x, dt, A, Bm, Cm, D_skip, z, dt_bias, h0, lengths = (
-                _to_device(t, dev) for t in (x, dt, A, Bm, Cm, D_skip, z, dt_bias, h0, lengths))
-        G, N = _scan_inputs(x, dt, A, Bm, Cm, D_skip, z, dt_bias, (B, T), dev)
-        _vector(h0, "h0", (B, D, N), dev)
-        _vector(lengths, "lengths", (B,), dev, torch.int32)
-        if y is None:
-            y = (torch.empty if lengths is None else torch.zeros)(x.shape, dtype=ty, device=dev)
-        else:
-            _vector(y, "y", x.shape, dev, ty)
-        if h_T is not None:
-            _vector(h_T, "h_T", (B, D, N), dev)
-        elif final_state:
-            h_T = torch.empty(B, D, N, dtype=torch.float32, device=dev)
-        L = lib()
-        size = L.gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N, _DTYPES[ty])
-        ws = _workspace(workspace, size, dev)
-        _check(L.gdr_ssm_scan_fwd(
-            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D_skip), _ptr(z), _ptr(dt_bias), _ptr(h0),
-            _ptr(lengths), _ptr(y), _ptr(h_T), _I64x10(*_scan_strides(x, dt, Bm, Cm, z)), B, T, D, G, N,
-            1 if dt_softplus else 0, _DTYPES[ty], _ptr(ws), size, handle), "gdr_ssm_scan_fwd")
-        return y, h_T
-
-    out = _scoped(dev, stream, body)
-    return tuple(_to_host(t) for t in out) if host else out
+    shape, ty = x.shape, x.dtype
+    B, T, D = shape
+    G, N = _scan_inputs(index, x, dt, A, Bm, Cm, D_skip, z, dt_bias)
+    if h0 is not None:
+        _dense(h0, "h0", (B, D, N), index)
+    if lengths is not None:
+        _dense(lengths, "lengths", (B,), index, _I32)
+    if y is None:
+        y = _new(shape, ty, index, lengths is not None)
+    else:
+        _dense(y, "y", shape, index, ty)
+    if h_T is not None:
+        _dense(h_T, "h_T", (B, D, N), index)
+    elif final_state:
+        h_T = _new((B, D, N), _F32, index)
+    L = lib()
+    size = L.gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N, _DTYPES[ty])
+    ws = _workspace(workspace, size, index)
+    strides = _I64x10(*x.stride()[:2], *dt.stride()[:2], *Bm.stride()[:2], *Cm.stride()[:2],
+                      *(z if z is not None else x).stride()[:2])
+    status = L.gdr_ssm_scan_fwd(
+        x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _ptr(D_skip), _ptr(z), _ptr(dt_bias),
+        _ptr(h0), _ptr(lengths), y.data_ptr(), _ptr(h_T), strides, B, T, D, G, N, 1 if dt_softplus else 0,
+        _DTYPES[ty], _ptr(ws), size, handle)
+    if status:
+        _check(status, "gdr_ssm_scan_fwd")
+    return y, h_T
 
 
 def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
@@ -332,30 +367,30 @@ def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.
     x, dt, z [B,D] and Bm, Cm [B,G,N] (rows may be strided), the rest as ``ssm_scan_fwd``.
     Returns y [B,D].
     """
-    ty = _type_of(x)
-    dev = x.device
-    if not x.is_cuda:
+    if isinstance(x, torch.Tensor) and not x.is_cuda:
         raise ValueError("ssm_scan_step works on CUDA tensors: the state is updated in place")
+    return _run(_scan_step, x, stream, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y)
+
+
+def _scan_step(handle, index, x, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y):
     if x.dim() != 2:
         raise ValueError("x must be [B,D]")
-    B, D = x.shape
-    G, N = _scan_inputs(x, dt, A, Bm, Cm, D_skip, z, dt_bias, (B,), dev)
-    if h is None:
-        raise TypeError("h must be a tensor")
-    _vector(h, "h", (B, D, N), dev)
-
-    def body(handle, y=y):
-        if y is None:
-            y = torch.empty(B, D, dtype=ty, device=dev)
-        else:
-            _vector(y, "y", (B, D), dev, ty)
-        strides = _I64x5(x.stride(0), dt.stride(0), Bm.stride(0), Cm.stride(0), 0 if z is None else z.stride(0))
-        _check(lib().gdr_ssm_scan_step(
-            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D_skip), _ptr(z), _ptr(dt_bias), _ptr(h), _ptr(y),
-            strides, B, D, G, N, 1 if dt_softplus else 0, _DTYPES[ty], handle), "gdr_ssm_scan_step")
-        return y
-
-    return _scoped(dev, stream, body)
+    shape, ty = x.shape, x.dtype
+    B, D = shape
+    G, N = _scan_inputs(index, x, dt, A, Bm, Cm, D_skip, z, dt_bias)
+    _dense(h, "h", (B, D, N), index)
+    if y is None:
+        y = torch.empty(shape, dtype=ty, device=index)
+    else:
+        _dense(y, "y", shape, index, ty)
+    strides = _I64x5(x.stride()[0], dt.stride()[0], Bm.stride()[0], Cm.stride()[0],
+                     0 if z is None else z.stride()[0])
+    status = lib().gdr_ssm_scan_step(
+        x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _ptr(D_skip), _ptr(z), _ptr(dt_bias),
+        h.data_ptr(), y.data_ptr(), strides, B, D, G, N, 1 if dt_softplus else 0, _DTYPES[ty], handle)
+    if status:
+        _check(status, "gdr_ssm_scan_step")
+    return y
 
 
 def ssm_scan_bwd_workspace_size(B, T, D, G=1, N=16, dtype=torch.bfloat16) -> int:
@@ -373,37 +408,37 @@ def ssm_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0), each in its input's shape and type
     (contiguous) and None where that input is; dx, ddt, dB, dC and dz are zero behind a row's end.
     """
-    ty = _type_of(x)
-    dev, host = _device(x), not x.is_cuda
+    return _run(_scan_bwd, x, stream, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace)
+
+
+def _scan_bwd(handle, index, x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace):
     if x.dim() != 3:
         raise ValueError("x must be [B,T,D]")
-    B, T, D = x.shape
-
-    def body(handle, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, dy=dy, D_skip=D_skip, z=z, dt_bias=dt_bias, h0=h0, dh_T=dh_T,
-             lengths=lengths):
-        if host:
-            x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, h0, dh_T, lengths = (
-                _to_device(t, dev) for t in (x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, h0, dh_T, lengths))
-        G, N = _scan_inputs(x, dt, A, Bm, Cm, D_skip, z, dt_bias, (B, T), dev)
-        _rows(dy, "dy", x.shape, ty, dev)
-        _vector(h0, "h0", (B, D, N), dev)
-        _vector(dh_T, "dh_T", (B, D, N), dev)
-        _vector(lengths, "lengths", (B,), dev, torch.int32)
-
-        def like(t, *shape, dtype=torch.float32):
-            return None if t is None else torch.empty(shape, dtype=dtype, device=dev)
-        dx, ddt, dz = (like(t, B, T, D, dtype=ty) for t in (x, dt, z))
-        dB, dC = (like(t, B, T, G, N, dtype=ty) for t in (Bm, Cm))
-        dA, dD, db, dh0 = like(A, D, N), like(D_skip, D), like(dt_bias, D), like(h0, B, D, N)
-        L = lib()
-        size = L.gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N, _DTYPES[ty])
-        ws = _workspace(workspace, size, dev)
-        _check(L.gdr_ssm_scan_bwd(
-            _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D_skip), _ptr(z), _ptr(dt_bias), _ptr(h0),
-            _ptr(lengths), _ptr(dy), _ptr(dh_T), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dz),
-            _ptr(db), _ptr(dh0), _I64x12(*_scan_strides(x, dt, Bm, Cm, z, dy)), B, T, D, G, N,
-            1 if dt_softplus else 0, _DTYPES[ty], _ptr(ws), size, handle), "gdr_ssm_scan_bwd")
-        return dx, ddt, dA, dB, dC, dD, dz, db, dh0
-
-    out = _scoped(dev, stream, body)
-    return tuple(_to_host(t) for t in out) if host else out
+    shape, ty = x.shape, x.dtype
+    B, T, D = shape
+    G, N = _scan_inputs(index, x, dt, A, Bm, Cm, D_skip, z, dt_bias)
+    _rows(dy, "dy", shape, index, ty)
+    if h0 is not None:
+        _dense(h0, "h0", (B, D, N), index)
+    if dh_T is not None:
+        _dense(dh_T, "dh_T", (B, D, N), index)
+    if lengths is not None:
+        _dense(lengths, "lengths", (B,), index, _I32)
+    dx, ddt, dz = _new(shape, ty, index), _new(shape, ty, index), None if z is None else _new(shape, ty, index)
+    dB, dC, dA = _new(Bm.shape, ty, index), _new(Bm.shape, ty, index), _new((D, N), _F32, index)
+    dD = None if D_skip is None else _new((D,), _F32, index)
+    db = None if dt_bias is None else _new((D,), _F32, index)
+    dh0 = None if h0 is None else _new((B, D, N), _F32, index)
+    L = lib()
+    size = L.gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N, _DTYPES[ty])
+    ws = _workspace(workspace, size, index)
+    strides = _I64x12(*x.stride()[:2], *dt.stride()[:2], *Bm.stride()[:2], *Cm.stride()[:2],
+                      *(z if z is not None else x).stride()[:2], *dy.stride()[:2])
+    status = L.gdr_ssm_scan_bwd(
+        x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _ptr(D_skip), _ptr(z), _ptr(dt_bias),
+        _ptr(h0), _ptr(lengths), dy.data_ptr(), _ptr(dh_T), dx.data_ptr(), ddt.data_ptr(), dA.data_ptr(),
+        dB.data_ptr(), dC.data_ptr(), _ptr(dD), _ptr(dz), _ptr(db), _ptr(dh0), strides, B, T, D, G, N,
+        1 if dt_softplus else 0, _DTYPES[ty], _ptr(ws), size, handle)
+    if status:
+        _check(status, "gdr_ssm_scan_bwd")
+    return dx, ddt, dA, dB, dC, dD, dz, db, dh0
