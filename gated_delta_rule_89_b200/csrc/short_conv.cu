@@ -23,29 +23,49 @@ namespace {
 constexpr int kConvThreads = 128;
 constexpr int kSms = 148;
 
+// A vector in memory as register pairs, and back.
+template <int VEC, typename V> __device__ __forceinline__ void widen(V v, typename Lanes<VEC>::P *p)
+{
+    float f[VEC];
+    unpack(v, f);
+    Lanes<VEC>::join(f, p);
+}
+template <int VEC, typename V> __device__ __forceinline__ V narrow(const typename Lanes<VEC>::P *p)
+{
+    float f[VEC];
+    Lanes<VEC>::split(p, f);
+    V v;
+    pack(v, f);
+    return v;
+}
+
 // The W taps of VEC neighbouring channels, and their biases.
 template <int VEC, int W>
-__device__ __forceinline__ void load_taps(const float *weight, const float *bias, int c0, float (&w)[W][VEC],
-                                          float (&b)[VEC])
+__device__ __forceinline__ void load_taps(const float *weight, const float *bias, int c0,
+                                          typename Lanes<VEC>::P (*w)[Lanes<VEC>::N], typename Lanes<VEC>::P *b)
 {
     const float *p = weight + (size_t)c0 * W;
+    float f[W][VEC], g[VEC];
     if (W == 4 && (reinterpret_cast<uintptr_t>(weight) & 15) == 0) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float4 q = *(const float4 *)(p + v * W);
-            w[0][v] = q.x;
-            w[1][v] = q.y;
-            w[2 < W ? 2 : 0][v] = q.z;
-            w[3 < W ? 3 : 0][v] = q.w;
+            f[0][v] = q.x;
+            f[1][v] = q.y;
+            f[2 < W ? 2 : 0][v] = q.z;
+            f[3 < W ? 3 : 0][v] = q.w;
         }
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][v] = p[v * W + j];
+            for (int j = 0; j < W; ++j) f[j][v] = p[v * W + j];
     }
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) b[v] = bias ? bias[c0 + v] : 0.f;
+    for (int v = 0; v < VEC; ++v) g[v] = bias ? bias[c0 + v] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) Lanes<VEC>::join(f[j], w[j]);
+    Lanes<VEC>::join(g, b);
 }
 
 // blockDim.x channel vectors by blockDim.y token runs; grid.x counts (batch,
@@ -132,32 +152,30 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
         }
     };
     fetch(now, left);
-    float w[W][VEC], bias[VEC], win[W - 1][VEC];
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    P w[W][L::N], bias[L::N], win[W - 1][L::N];
     load_taps<VEC, W>(a.weight, a.bias, c0, w, bias);
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) unpack(before[i], win[i]);
+    for (int i = 0; i < W - 1; ++i) widen<VEC>(before[i], win[i]);
     for (; left > 0; left -= U) {
         fetch(next, left - U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float cur[VEC], acc[VEC];
-            unpack(now[u], cur);
+            P cur[L::N], acc[L::N];
+            widen<VEC>(now[u], cur);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                float s = bias[v];
+            for (int v = 0; v < L::N; ++v) {
+                P s = bias[v];
 #pragma unroll
-                for (int i = 0; i < W - 1; ++i) s = fmaf(w[i][v], win[i][v], s);
-                s = fmaf(w[W - 1][v], cur[v], s);
-                acc[v] = a.silu ? s * sigmoid_f32(s) : s;
+                for (int i = 0; i < W - 1; ++i) s = fma2(w[i][v], win[i][v], s);
+                s = fma2(w[W - 1][v], cur[v], s);
+                acc[v] = a.silu ? mul2(s, sigmoid2(s)) : s;
 #pragma unroll
                 for (int i = 0; i + 1 < W - 1; ++i) win[i][v] = win[i + 1][v];
                 win[W - 2][v] = cur[v];
             }
-            if (u < left) {
-                V out;
-                pack(out, acc);
-                *(V *)y = out;
-            }
+            if (u < left) *(V *)y = narrow<VEC, V>(acc);
             y += a.d;
             now[u] = next[u];
         }
@@ -185,28 +203,28 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a)
         for (int i = 0; i < W - 1; ++i) rows[r][i] = *(const V *)(st + (size_t)i * D);
         rows[r][W - 1] = *(const V *)((const T *)a.x + (b0 + r) * a.xs.b + c0);
     }
-    float w[W][VEC], bias[VEC];
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    P w[W][L::N], bias[L::N];
     load_taps<VEC, W>(a.weight, a.bias, c0, w, bias);
 #pragma unroll
     for (int r = 0; r < kStepRows; ++r) {
         if (b0 + r >= a.B) break;
-        float acc[VEC];
+        P acc[L::N];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) acc[v] = bias[v];
+        for (int v = 0; v < L::N; ++v) acc[v] = bias[v];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float f[VEC];
-            unpack(rows[r][i], f);
+            P f[L::N];
+            widen<VEC>(rows[r][i], f);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) acc[v] = fmaf(w[i][v], f[v], acc[v]);
+            for (int v = 0; v < L::N; ++v) acc[v] = fma2(w[i][v], f[v], acc[v]);
         }
         if (a.silu) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) acc[v] *= sigmoid_f32(acc[v]);
+            for (int v = 0; v < L::N; ++v) acc[v] = mul2(acc[v], sigmoid2(acc[v]));
         }
-        V out;
-        pack(out, acc);
-        *(V *)((T *)a.y + (size_t)(b0 + r) * D + c0) = out;
+        *(V *)((T *)a.y + (size_t)(b0 + r) * D + c0) = narrow<VEC, V>(acc);
         T *st = (T *)a.state_out + (size_t)(b0 + r) * (W - 1) * D + c0;
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) *(V *)(st + (size_t)i * D) = rows[r][i + 1];
@@ -235,7 +253,9 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
     const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const int b = (int)(piece / runs);
-    float dw[W][VEC] = {}, db[VEC] = {};
+    using L = Lanes<VEC>;
+    using P = typename L::P;
+    P dw[W][L::N] = {}, db[L::N] = {};   // all bits 0 is 0
 
     if (c0 < D && b < a.B) {
         const int t0 = (int)(piece - (long long)b * runs) * run;
@@ -250,18 +270,14 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a
         const T *dso = a.dstate_out ? (const T *)a.dstate_out + (size_t)b * (W - 1) * D + c0 : nullptr;
         T *dst = a.dstate ? (T *)a.dstate + (size_t)b * (W - 1) * D + c0 : nullptr;
 
-        float w[W][VEC], bias[VEC], win[W - 1][VEC], dp[W][VEC];
+        P w[W][L::N], bias[L::N], win[W - 1][L::N], dp[W][L::N] = {};
         load_taps<VEC, W>(a.weight, a.bias, c0, w, bias);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v)
-#pragma unroll
-            for (int j = 0; j < W; ++j) dp[j][v] = 0.f;
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             const int r = t0 - (W - 1) + i;
             V v = r >= 0 ? (r < len ? *(const V *)(x + r * a.xs.t) : zero_pack<V>())
                          : (st ? *(const V *)(st + (size_t)(W - 1 + r) * D) : zero_pack<V>());
-            unpack(v, win[i]);
+            widen<VEC>(v, win[i]);
         }
         // rows the walk completes: [-(W-1), t1) from a row's first run, [t0, t1) from the others
         const int tend = t1 + (W - 1), live_end = min(len, tend), rmin = first ? -(W - 1) : t0;
@@ -284,33 +300,33 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int tt = t + u;
-                float cur[VEC], g[VEC], out[VEC];
-                unpack(xin[u], cur);
-                unpack(gin[u], g);
+                P cur[L::N], g[L::N], out[L::N];
+                widen<VEC>(xin[u], cur);
+                widen<VEC>(gin[u], g);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float s = bias[v];
+                for (int v = 0; v < L::N; ++v) {
+                    P s = bias[v];
 #pragma unroll
-                    for (int i = 0; i < W - 1; ++i) s = fmaf(w[i][v], win[i][v], s);
-                    s = fmaf(w[W - 1][v], cur[v], s);
-                    float p = g[v];
-                    if (a.silu) {
-                        const float q = sigmoid_f32(s);
-                        p *= fmaf(s * q, 1.f - q, q);
+                    for (int i = 0; i < W - 1; ++i) s = fma2(w[i][v], win[i][v], s);
+                    s = fma2(w[W - 1][v], cur[v], s);
+                    P p = g[v];
+                    if (a.silu) {   // q + s q (1 - q)
+                        const P q = sigmoid2(s);
+                        p = mul2(p, fma2(mul2(s, q), fma2(q, L::all(-1.f), L::all(1.f)), q));
                     }
-                    if (!FULL && tt >= live_end) p = 0.f;
+                    if (!FULL && tt >= live_end) p = L::all(0.f);
 #pragma unroll
                     for (int i = 0; i < W - 1; ++i) dp[i][v] = dp[i + 1][v];
                     dp[W - 1][v] = p;
                     if (FULL || tt < t1) {
 #pragma unroll
-                        for (int i = 0; i < W - 1; ++i) dw[i][v] = fmaf(p, win[i][v], dw[i][v]);
-                        dw[W - 1][v] = fmaf(p, cur[v], dw[W - 1][v]);
-                        db[v] += p;
+                        for (int i = 0; i < W - 1; ++i) dw[i][v] = fma2(p, win[i][v], dw[i][v]);
+                        dw[W - 1][v] = fma2(p, cur[v], dw[W - 1][v]);
+                        db[v] = add2(db[v], p);
                     }
-                    float acc = w[0][v] * dp[W - 1][v];
+                    P acc = mul2(w[0][v], dp[W - 1][v]);
 #pragma unroll
-                    for (int j = 1; j < W; ++j) acc = fmaf(w[j][v], dp[W - 1 - j][v], acc);
+                    for (int j = 1; j < W; ++j) acc = fma2(w[j][v], dp[W - 1 - j][v], acc);
                     out[v] = acc;
 #pragma unroll
                     for (int i = 0; i + 1 < W - 1; ++i) win[i][v] = win[i + 1][v];
@@ -319,13 +335,12 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a
                 const int r = tt - (W - 1);
                 if (FULL || (r >= rmin && r < t1)) {
                     if (!FULL && dso && r >= len - (W - 1) && r < len) {
-                        float f[VEC];
-                        unpack(*(const V *)(dso + (size_t)(r - len + W - 1) * D), f);
+                        P f[L::N];
+                        widen<VEC>(*(const V *)(dso + (size_t)(r - len + W - 1) * D), f);
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) out[v] += f[v];
+                        for (int v = 0; v < L::N; ++v) out[v] = add2(out[v], f[v]);
                     }
-                    V o;
-                    pack(o, out);
+                    const V o = narrow<VEC, V>(out);
                     if (FULL || r >= 0) *(V *)dxr = o;
                     else if (dst) *(V *)(dst + (size_t)(r + W - 1) * D) = o;
                 }
@@ -350,8 +365,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) sum[tid][v] = j < W ? dw[j < W ? j : 0][v] : db[v];
+        L::split(j < W ? dw[j < W ? j : 0] : db, sum[tid]);
         __syncthreads();
         if (threadIdx.y == 0 && c0 < D) {
             for (int k = 1; k < (int)blockDim.y; ++k)

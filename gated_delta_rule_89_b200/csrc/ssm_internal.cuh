@@ -143,6 +143,40 @@ __device__ __forceinline__ f32x2 exp2_approx2(f32x2 x)
 {
     return make_f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
 }
+// The same operations on one value, for code written for either.
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sigmoid2(float x) { return sigmoid_f32(x); }
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x)
+{
+    const f32x2 d = add2(exp2_approx2(mul2(x, both(-kLog2e))), both(1.f));
+    return make_f32x2(rcp_approx(lo_f32(d)), rcp_approx(hi_f32(d)));
+}
+// VEC values as register pairs, or one value.
+template <int VEC> struct Lanes {
+    using P = f32x2;
+    static constexpr int N = VEC / 2;
+    static __device__ __forceinline__ P all(float v) { return both(v); }
+    static __device__ __forceinline__ void join(const float *f, P *p)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = make_f32x2(f[2 * i], f[2 * i + 1]);
+    }
+    static __device__ __forceinline__ void split(const P *p, float *f)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[2 * i] = lo_f32(p[i]), f[2 * i + 1] = hi_f32(p[i]);
+    }
+};
+template <> struct Lanes<1> {
+    using P = float;
+    static constexpr int N = 1;
+    static __device__ __forceinline__ P all(float v) { return v; }
+    static __device__ __forceinline__ void join(const float *f, P *p) { p[0] = f[0]; }
+    static __device__ __forceinline__ void split(const P *p, float *f) { f[0] = p[0]; }
+};
+
 // The decay 2^(delta A2) of a state, and of two.  The hardware's 2^x lies below the
 // exact value by 2e-8 at the mean where it is close to 1, and a slowly
 // decaying state multiplies a thousand of them; raising the exponent by 2e-8

@@ -126,6 +126,7 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
             h[k][0] = make_f32x2(r.x, r.y);
             h[k][1] = make_f32x2(r.z, r.w);
             if ((MODE == FULL || MODE == POINTS) && on[k])
+#pragma unroll 4
                 for (int s = 1; s <= piece; ++s) {   // fold in the pieces ahead
                     const f32x2 sum = both(pc.sums[((size_t)s * a.B + b) * a.D + cfirst + ch + k]);
                     const ulonglong2 v = *(const ulonglong2 *)(pc.slots + s * slot + ak);
@@ -478,7 +479,7 @@ Pieces plan(int B, int T, int D, int G, int N, void *workspace)
     const long long blocks = (long long)B * G * blocks_per_group(D, G, N, channels_per_thread(B, D, G, N));
     if (blocks > 0 && blocks * 2 <= kSms && T >= 8 * kTile) {
         long long count = 2 * kSms / blocks;
-        if (count > T / (4 * kTile)) count = T / (4 * kTile);
+        if (count > T / (2 * kTile)) count = T / (2 * kTile);
         p.tokens = (int)((T + count - 1) / count + kTile - 1) / kTile * kTile;
         p.count = (T + p.tokens - 1) / p.tokens;
     }

@@ -43,7 +43,7 @@ template <typename T, int N> struct Shape {
     static constexpr int LN = N / 4;                   // lanes of a channel
     static constexpr int CL = 32 / LN;                 // channels of a warp
     static constexpr int CB = kWarps * CL;             // channels of a block
-    static constexpr int kTile = N == 64 ? 8 : 16;     // tokens between two block barriers
+    static constexpr int kTile = N == 16 || N == 32 ? 16 : 8;   // tokens between two block barriers
     static constexpr int GR = CB / 4;
     static constexpr int TPP = kHelpers / GR;
     static constexpr int R = TPP >= kTile ? 1 : kTile / TPP;
@@ -123,6 +123,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
         f32x2 carry0 = make_f32x2(r4.x, r4.y), carry1 = make_f32x2(r4.z, r4.w), dA0 = 0, dA1 = 0;
         // fold in the pieces behind, the last that the row has first
         if (pc.count > 1 && on)
+#pragma unroll 4
             for (int s = (len - 1) / pc.tokens; s > piece; --s) {
                 const f32x2 sum = both(pc.sums[((size_t)s * f.B + b) * f.D + c]);
                 const ulonglong2 v = *(const ulonglong2 *)(pc.slots + (size_t)s * f.B * f.D * N + at);
@@ -513,9 +514,9 @@ BackPieces plan(int B, int T, int D, int G, int N)
 {
     BackPieces p = {1, T > 0 ? T : 1, nullptr, nullptr};
     const long long blocks = (long long)B * G * blocks_per_group(D, G, N);
-    if (blocks > 0 && blocks * 2 <= kSms && T >= 256) {
+    if (blocks > 0 && blocks * 2 <= kSms && T >= 96) {
         long long count = kSms / blocks;
-        if (count > T / 128) count = T / 128;
+        if (count > T / 32) count = T / 32;
         p.tokens = (int)((T + count - 1) / count + 31) / 32 * 32;
         p.count = (T + p.tokens - 1) / p.tokens;
     }
