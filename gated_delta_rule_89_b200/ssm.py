@@ -33,20 +33,19 @@ _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _run(call, x, stream, *args):
+def _run(call, x, stream, args):
     """call(stream handle, device index, x, *args) with the device and the stream current that it
     runs on, so that what it allocates belongs to that stream.  A host x: every tensor is copied
     to the current device first and the results back afterwards."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
-    if x.is_cuda:
-        index = x.get_device()
-        if stream is None and index == _current_device():
-            return call(_current_stream(index), index, x, *args)
-        host = False
-    else:
+    index = x.get_device()
+    host = index < 0
+    if host:
         _type_of(x)
-        index, host = torch.cuda.current_device(), True
+        index = torch.cuda.current_device()
+    elif stream is None and index == _current_device():
+        return call(_current_stream(index), index, x, *args)
     dev = torch.device("cuda", index)
     if stream is None:
         with torch.cuda.device(dev):
@@ -147,15 +146,21 @@ def _conv_strides(x):
 
 def _conv_params(weight, bias, activation, D, index):
     """Checks weight and bias; returns (taps, the activation's number)."""
-    if activation not in _ACTIVATIONS:
-        raise ValueError("activation must be None or 'silu'")
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError(f"weight must be a tensor [{D},W]")
-    W = weight.shape[1]
-    _dense(weight, "weight", (D, W), index)
+    try:
+        act = _ACTIVATIONS[activation]
+    except (KeyError, TypeError):
+        raise ValueError("activation must be None or 'silu'") from None
+    try:
+        rows, W = weight.shape
+        if rows != D or weight.dtype is not _F32 or weight.get_device() != index or not weight.is_contiguous():
+            raise ValueError
+    except (AttributeError, ValueError):
+        if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+            raise ValueError(f"weight must be a tensor [{D},W]") from None
+        _refuse(weight, "weight", (D, weight.shape[1]), index, _F32)
     if bias is not None:
         _dense(bias, "bias", (D,), index)
-    return W, _ACTIVATIONS[activation]
+    return W, act
 
 
 def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -170,7 +175,7 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     activation "silu" or None; lengths int32 [B].  Returns (y, contiguous in x's shape and
     type, and the state after the prompt or None); ``state_out`` may be ``state``.
     """
-    return _run(_conv_fwd, x, stream, weight, bias, state, activation, lengths, y, state_out, final_state)
+    return _run(_conv_fwd, x, stream, (weight, bias, state, activation, lengths, y, state_out, final_state))
 
 
 def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, y, state_out, final_state):
@@ -207,26 +212,31 @@ def short_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, 
     x [B,D] (rows may be strided); state [B,W-1,D] in x's type is shifted IN PLACE; weight, bias
     and activation as ``short_conv_fwd``.  Returns y [B,D].
     """
-    if isinstance(x, torch.Tensor) and not x.is_cuda:
+    if isinstance(x, torch.Tensor) and x.get_device() < 0:
         raise ValueError("short_conv_step works on CUDA tensors: the state is updated in place")
-    return _run(_conv_step, x, stream, state, weight, bias, activation, y)
+    return _run(_conv_step, x, stream, (state, weight, bias, activation, y))
 
 
 def _conv_step(handle, index, x, state, weight, bias, activation, y):
-    dt = _type_of(x)
-    if x.dim() != 2:
+    dt, shape = x.dtype, x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [B,D]")
-    shape = x.shape
+    code = _DTYPES.get(dt)
+    if code is None:
+        _type_of(x)
     B, D = shape
-    _rows(x, "x", shape, index, dt)
+    xs = D
+    if not x.is_contiguous():
+        _rows(x, "x", shape, index, dt)
+        xs = x.stride()[0]
     W, act = _conv_params(weight, bias, activation, D, index)
     _dense(state, "state", (B, W - 1, D), index, dt)
     if y is None:
         y = torch.empty(shape, dtype=dt, device=index)
     else:
         _dense(y, "y", shape, index, dt)
-    status = lib().gdr_short_conv_step(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), y.data_ptr(),
-                                       x.stride()[0], B, D, W, act, _DTYPES[dt], handle)
+    status = lib().gdr_short_conv_step(x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                                       state.data_ptr(), y.data_ptr(), xs, B, D, W, act, code, handle)
     if status:
         _check(status, "gdr_short_conv_step")
     return y
@@ -244,7 +254,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias
     state).  dx has x's shape and its order in memory (token rows stay token rows); it is
     zero behind a row's end.
     """
-    return _run(_conv_bwd, x, stream, weight, dy, bias, state, dstate_out, activation, lengths, workspace)
+    return _run(_conv_bwd, x, stream, (weight, dy, bias, state, dstate_out, activation, lengths, workspace))
 
 
 def _conv_bwd(handle, index, x, weight, dy, bias, state, dstate_out, activation, lengths, workspace):
@@ -291,8 +301,9 @@ def _scan_inputs(index, x, dt, A, Bm, Cm, D_skip, z, dt_bias):
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(shape) + 1:
         raise ValueError(f"Bm and Cm must be [{'B,T' if len(shape) == 3 else 'B'},G,N]")
     lead = Bm.shape
-    G, N, D = lead[-2], lead[-1], shape[-1]
-    if lead[:-2] != shape[:-1] or G < 1 or D % G:
+    *rows, G, N = lead
+    D = shape[-1]
+    if tuple(rows) != shape[:-1] or G < 1 or D % G:
         raise ValueError(f"Bm {list(lead)} does not fit x {list(shape)}: [..., G, N] with G dividing {D}")
     _rows(Bm, "Bm", lead, index, ty, 2)
     _rows(Cm, "Cm", lead, index, ty, 2)
@@ -321,8 +332,8 @@ def ssm_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     A [D,N], D_skip [D], dt_bias [D], h0 [B,D,N] fp32; N in 8, 16, 32, 64; lengths int32 [B].
     Returns (y [B,T,D] in x's type, h_T [B,D,N] fp32 or None); ``h_T`` may be ``h0``.
     """
-    return _run(_scan_fwd, x, stream, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T,
-                final_state, workspace)
+    return _run(_scan_fwd, x, stream, (dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T,
+                final_state, workspace))
 
 
 def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T, final_state,
@@ -367,9 +378,9 @@ def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.
     x, dt, z [B,D] and Bm, Cm [B,G,N] (rows may be strided), the rest as ``ssm_scan_fwd``.
     Returns y [B,D].
     """
-    if isinstance(x, torch.Tensor) and not x.is_cuda:
+    if isinstance(x, torch.Tensor) and x.get_device() < 0:
         raise ValueError("ssm_scan_step works on CUDA tensors: the state is updated in place")
-    return _run(_scan_step, x, stream, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y)
+    return _run(_scan_step, x, stream, (dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y))
 
 
 def _scan_step(handle, index, x, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y):
@@ -408,7 +419,7 @@ def ssm_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0), each in its input's shape and type
     (contiguous) and None where that input is; dx, ddt, dB, dC and dz are zero behind a row's end.
     """
-    return _run(_scan_bwd, x, stream, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace)
+    return _run(_scan_bwd, x, stream, (dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace))
 
 
 def _scan_bwd(handle, index, x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace):

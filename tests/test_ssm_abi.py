@@ -110,12 +110,12 @@ def test_scan_bwd_arguments(L):
     for bad in (dict(A=P(0x100008)), dict(dA=P(0x100008)), dict(dh0=P(0x100004)), dict(dD=P(0x100002)),
                 dict(dx=P(0x100001)), dict(ws=P(0x100008))):
         assert bwd(**bad) == ALIGN, bad
-    need = L.gdr_ssm_scan_bwd_workspace_size(2, 100, 64, 1, 16, 1)
+    need = L.gdr_ssm_scan_bwd_workspace_size(2, 90, 64, 1, 16, 1)
     # states every 8 tokens, the one block's parts of dB and dC, dA, dD and ddt_bias per row, and
     # what the forward pass wants
     up = lambda n: (n + 255) // 256 * 256   # noqa: E731
-    assert need == up(2 * 13 * 64 * 16 * 4) + up(2 * 100 * 32 * 4) + up(2 * 64 * 16 * 4) + up(2 * 64 * 2 * 4) + \
-        L.gdr_ssm_scan_fwd_workspace_size(2, 100, 64, 1, 16, 1)
+    assert need == up(2 * 12 * 64 * 16 * 4) + up(2 * 90 * 32 * 4) + up(2 * 64 * 16 * 4) + up(2 * 64 * 2 * 4) + \
+        L.gdr_ssm_scan_fwd_workspace_size(2, 90, 64, 1, 16, 1)
     assert bwd(D=0) == OK
 
 
