@@ -74,12 +74,12 @@ def lib() -> ctypes.CDLL:
         L.gdr2_recurrent_step.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P]
         L.gdr2_recurrent_step.restype = I
         S = ctypes.c_longlong
-        L.gdr_short_conv_fwd.argtypes = [P] * 8 + [I] * 7 + [P]
+        L.gdr_short_conv_fwd.argtypes = [P] * 8 + [I] * 8 + [P]
         L.gdr_short_conv_step.argtypes = [P] * 5 + [S] + [I] * 5 + [P]
         L.gdr_short_conv_bwd.argtypes = [P] * 14 + [I] * 7 + [P, Z, P]
         L.gdr_short_conv_bwd_workspace_size.argtypes = [I] * 6
         L.gdr_short_conv_bwd_workspace_size.restype = Z
-        L.gdr_ssm_scan_fwd.argtypes = [P] * 13 + [I] * 7 + [P, Z, P]
+        L.gdr_ssm_scan_fwd.argtypes = [P] * 13 + [I] * 8 + [P, Z, P]
         L.gdr_ssm_scan_fwd_workspace_size.argtypes = [I] * 6
         L.gdr_ssm_scan_fwd_workspace_size.restype = Z
         L.gdr_ssm_scan_bwd.argtypes = [P] * 22 + [I] * 7 + [P, Z, P]

@@ -501,7 +501,7 @@ int nothing_to_do()
 }  // namespace
 
 GDR_API int gdr_short_conv_fwd(const void *x, const float *weight, const float *bias, const void *state,
-                               const int *lengths, void *y, void *state_out, const long long *x_strides,
+                               const int *lengths, void *y, void *state_out, const long long *x_strides, int zero_tail,
                                int B, int H, int T, int d, int W, int act, int dtype, void *stream)
 {
     if (const int e = conv_sizes(B, H, T, d, W, act, dtype)) return e;
@@ -511,7 +511,7 @@ GDR_API int gdr_short_conv_fwd(const void *x, const float *weight, const float *
     const void *rows[] = {x, state, y, state_out}, *words[] = {weight, bias, lengths};
     if (any_misaligned(rows, 4, elem_bytes(dtype)) || any_misaligned(words, 3, 4)) return GDR_ERR_ALIGNMENT;
     gdr::ConvArgs a = {x, rows_or_dense(x_strides, H, T, d), weight, bias, state, lengths, y, state_out,
-                       B, H, T, d, W, act == GDR_ACT_SILU, dtype == GDR_BF16};
+                       B, H, T, d, W, act == GDR_ACT_SILU, dtype == GDR_BF16, lengths && zero_tail};
     int launches = 0;
     const cudaError_t e = gdr::launch_short_conv_fwd(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -527,7 +527,7 @@ GDR_API int gdr_short_conv_step(const void *x, const float *weight, const float 
     const void *rows[] = {x, state, y}, *words[] = {weight, bias};
     if (any_misaligned(rows, 3, elem_bytes(dtype)) || any_misaligned(words, 2, 4)) return GDR_ERR_ALIGNMENT;
     gdr::ConvArgs a = {x, {x_stride, 0, 0}, weight, bias, state, nullptr, y, state,
-                       B, 1, 1, D, W, act == GDR_ACT_SILU, dtype == GDR_BF16};
+                       B, 1, 1, D, W, act == GDR_ACT_SILU, dtype == GDR_BF16, false};
     int launches = 0;
     const cudaError_t e = gdr::launch_short_conv_step(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -579,7 +579,7 @@ GDR_API size_t gdr_ssm_scan_fwd_workspace_size(int B, int T, int D, int G, int N
 
 GDR_API int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
                              const float *D_skip, const void *z, const float *dt_bias, const float *h0,
-                             const int *lengths, void *y, float *h_T, const long long *strides,
+                             const int *lengths, void *y, float *h_T, const long long *strides, int zero_tail,
                              int B, int T, int D, int G, int N, int dt_softplus, int dtype,
                              void *workspace, size_t ws_bytes, void *stream)
 {
@@ -599,7 +599,7 @@ GDR_API int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, cons
                        tokens_or_dense(s ? s + 4 : s, T, (long long)G * N),
                        tokens_or_dense(s ? s + 6 : s, T, (long long)G * N), tokens_or_dense(s ? s + 8 : s, T, D),
                        A, D_skip, dt_bias, h0, lengths, y, h_T, B, T, D, G, N, dt_softplus != 0, dtype == GDR_BF16,
-                       workspace};
+                       workspace, lengths && zero_tail};
     int launches = 0;
     const cudaError_t e = gdr::launch_ssm_scan_fwd(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -622,7 +622,7 @@ GDR_API int gdr_ssm_scan_step(const void *x, const void *dt, const float *A, con
     const long long *s = strides ? strides : dense;
     gdr::ScanArgs a = {x, dt, Bm, Cm, z, {s[0], 0}, {s[1], 0}, {s[2], 0}, {s[3], 0}, {s[4], 0},
                        A, D_skip, dt_bias, nullptr, nullptr, y, h, B, 1, D, G, N, dt_softplus != 0,
-                       dtype == GDR_BF16, nullptr};
+                       dtype == GDR_BF16, nullptr, false};
     int launches = 0;
     const cudaError_t e = gdr::launch_ssm_scan_step(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -666,7 +666,7 @@ GDR_API int gdr_ssm_scan_bwd(const void *x, const void *dt, const float *A, cons
         {x, dt, Bm, Cm, z, tokens_or_dense(s, T, D), tokens_or_dense(s ? s + 2 : s, T, D),
          tokens_or_dense(s ? s + 4 : s, T, (long long)G * N), tokens_or_dense(s ? s + 6 : s, T, (long long)G * N),
          tokens_or_dense(s ? s + 8 : s, T, D), A, D_skip, dt_bias, h0, lengths, nullptr, nullptr, B, T, D, G, N,
-         dt_softplus != 0, dtype == GDR_BF16, nullptr},
+         dt_softplus != 0, dtype == GDR_BF16, nullptr, false},
         dy, tokens_or_dense(s ? s + 10 : s, T, D), dh_T, dx, ddt, dB, dC, z ? dz : nullptr, dA, dD, ddt_bias, dh0,
         workspace};
     int launches = 0;

@@ -138,6 +138,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
             *(V *)(so + (size_t)i * D) = v;
         }
     }
+    if (a.zero_tail) {
+        T *tail = (T *)a.y + ((size_t)b * a.H + head) * a.T * a.d + j0;
+        for (int t = max(t0, len); t < min(t0 + run, a.T); ++t) *(V *)(tail + (size_t)t * a.d) = zero_pack<V>();
+    }
     int left = min(t0 + run, len) - t0;
     if (left <= 0) return;
 

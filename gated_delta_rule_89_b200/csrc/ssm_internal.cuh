@@ -22,6 +22,7 @@ struct ConvArgs {
     void *y, *state_out;          // [B, H, T, d]; [B, W-1, D] or NULL
     int B, H, T, d, W;
     bool silu, bf16;
+    bool zero_tail;               // y is set to zero behind a row's end (otherwise left as it is)
 };
 
 struct ConvBwdArgs {
@@ -57,6 +58,7 @@ struct ScanArgs {
     int B, T, D, G, N;
     bool softplus, bf16;
     void *workspace;                              // ssm_scan_fwd_workspace_bytes()
+    bool zero_tail;                               // as ConvArgs
 };
 
 cudaError_t launch_ssm_scan_fwd(const ScanArgs &a, cudaStream_t stream, int *launches);
@@ -303,7 +305,7 @@ __device__ __forceinline__ int row_length(const int *lengths, int b, int T)
 __device__ __forceinline__ float4 load_if(const float4 *p, bool on)
 {
     float4 v;
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
         "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w) : "l"(p), "r"((int)on));
     return v;
@@ -311,7 +313,7 @@ __device__ __forceinline__ float4 load_if(const float4 *p, bool on)
 __device__ __forceinline__ uint4 load_if(const uint4 *p, bool on)
 {
     uint4 v;
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
         "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)on));
     return v;
@@ -319,7 +321,7 @@ __device__ __forceinline__ uint4 load_if(const uint4 *p, bool on)
 __device__ __forceinline__ uint2 load_if(const uint2 *p, bool on)
 {
     uint2 v;
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
         "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
         : "=&r"(v.x), "=&r"(v.y) : "l"(p), "r"((int)on));
     return v;
@@ -327,14 +329,14 @@ __device__ __forceinline__ uint2 load_if(const uint2 *p, bool on)
 __device__ __forceinline__ float load_if(const float *p, bool on)
 {
     float v;
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
         : "=&f"(v) : "l"(p), "r"((int)on));
     return v;
 }
 __device__ __forceinline__ unsigned short load_if(const unsigned short *p, bool on)
 {
     unsigned short v;
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
         : "=&h"(v) : "l"(p), "r"((int)on));
     return v;
 }

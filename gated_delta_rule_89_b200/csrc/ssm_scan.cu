@@ -90,6 +90,12 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
     constexpr bool kBack = MODE == ADJOINT;
     const int len = row_length(a.lengths, b, a.T);
     const int t0 = piece * pc.tokens, t1 = min(t0 + pc.tokens, len);
+    if (MODE == FULL && a.zero_tail) {                        // the piece's tokens behind the row's end
+        const int stop = min(t0 + pc.tokens, a.T), from = max(t0, len), wide = cend - cfirst;
+        T *y = (T *)a.y + ((size_t)b * a.T + from) * a.D + cfirst;
+        for (long long k = threadIdx.x; k < (long long)(stop - from) * wide; k += S::THREADS)
+            y[k / wide * a.D + k % wide] = from_f32<T>(0.f);
+    }
     if (piece > 0 && t0 >= t1) return;                        // the whole block
     const int tiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;
     const int tid = threadIdx.x;

@@ -81,6 +81,64 @@ struct BwdParts {
     BackPieces pc;
 };
 
+// A lane's 4 states in the order in which the exchange between the lanes gives
+// them away: position j holds state j ^ order, the bits of `order` being the
+// lane's bits of the first two steps.  Then "keep half, send half" is the same
+// registers in every lane, and no value has to be selected.
+struct Order {
+    int first;                 // 2 * bit 1 of the order: where the pair of positions 0, 1 lies
+    bool swap;                 // bit 0: the two of a pair change places
+    unsigned low, high;        // byte selectors that widen the bf16 of positions 0 and 1 of a pair
+    __device__ Order(int order)
+        : first(order & 2), swap(order & 1), low(swap ? 0x3244u : 0x1044u), high(swap ? 0x1044u : 0x3244u) {}
+    __device__ __forceinline__ int state(int j) const { return j ^ (first | (int)swap); }
+    __device__ __forceinline__ f32x2 pair(float2 v) const { return swap ? make_f32x2(v.y, v.x) : make_f32x2(v.x, v.y); }
+    // both pairs of 4 values in memory, and back
+    __device__ __forceinline__ void load(const float *p, f32x2 &a, f32x2 &b) const
+    {
+        a = pair(*(const float2 *)(p + first));
+        b = pair(*(const float2 *)(p + (first ^ 2)));
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, f32x2 &a, f32x2 &b) const
+    {
+        const unsigned u = *(const unsigned *)(p + first), v = *(const unsigned *)(p + (first ^ 2));
+        a = make_f32x2(__uint_as_float(__byte_perm(u, 0, low)), __uint_as_float(__byte_perm(u, 0, high)));
+        b = make_f32x2(__uint_as_float(__byte_perm(v, 0, low)), __uint_as_float(__byte_perm(v, 0, high)));
+    }
+    __device__ __forceinline__ void store(float *p, f32x2 a, f32x2 b) const
+    {
+        *(f32x2 *)(p + first) = pair(make_float2(lo_f32(a), hi_f32(a)));
+        *(f32x2 *)(p + (first ^ 2)) = pair(make_float2(lo_f32(b), hi_f32(b)));
+    }
+};
+
+// The sums of 4 values of dB and 4 of dC, in a lane's order, over the channels
+// of a warp (lanes LN, 2 LN, ... apart), stored by the lane that has them.
+template <int N, int LN, int CL>
+__device__ __forceinline__ void store_sums(f32x2 dB0, f32x2 dB1, f32x2 dC0, f32x2 dC1, int lane, const Order &order,
+                                           float *out)
+{
+    constexpr unsigned all = 0xffffffffu;
+    float b0 = lo_f32(dB0) + __shfl_xor_sync(all, lo_f32(dB1), LN), b1 = hi_f32(dB0) + __shfl_xor_sync(all, hi_f32(dB1), LN);
+    float c0 = lo_f32(dC0) + __shfl_xor_sync(all, lo_f32(dC1), LN), c1 = hi_f32(dC0) + __shfl_xor_sync(all, hi_f32(dC1), LN);
+    if constexpr (CL == 2) {
+        *(float2 *)(out + order.state(0)) = make_float2(b0, b1);
+        *(float2 *)(out + N + order.state(0)) = make_float2(c0, c1);
+    } else {
+        b0 += __shfl_xor_sync(all, b1, 2 * LN);
+        c0 += __shfl_xor_sync(all, c1, 2 * LN);
+        if constexpr (CL == 4) {
+            out[order.state(0)] = b0;
+            out[N + order.state(0)] = c0;
+        } else {
+            const bool up = lane & (4 * LN);
+            float v = (up ? c0 : b0) + __shfl_xor_sync(all, up ? b0 : c0, 4 * LN);
+            if constexpr (CL == 16) v += __shfl_xor_sync(all, v, 8 * LN);
+            if (CL == 8 || lane < 16) out[(up ? N : 0) + order.state(0)] = v;
+        }
+    }
+}
+
 template <typename T, int N, bool VECTOR>
 __global__ void __launch_bounds__(kThreads, 1)
 ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
@@ -114,28 +172,33 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
         const int ch = warp * S::CL + lane / S::LN, c = cfirst + ch;
         const bool on = c < cend;
         const size_t at = ((size_t)b * f.D + c) * N + n0;
-        float4 q4 = make_float4(0.f, 0.f, 0.f, 0.f), r4 = q4;
+        const Order order(((lane / S::LN) & 1) * 2 + (S::CL >= 4 ? (lane / (2 * S::LN)) & 1 : 0));
+        f32x2 A0 = 0, A1 = 0, carry0 = 0, carry1 = 0, dA0 = 0, dA1 = 0;
         if (on) {
-            q4 = *(const float4 *)(f.A + (size_t)c * N + n0);
-            if (a.dh_T) r4 = *(const float4 *)(a.dh_T + at);
+            order.load(f.A + (size_t)c * N + n0, A0, A1);
+            if (a.dh_T) order.load(a.dh_T + at, carry0, carry1);
         }
-        const f32x2 A0 = make_f32x2(q4.x * kLog2e, q4.y * kLog2e), A1 = make_f32x2(q4.z * kLog2e, q4.w * kLog2e);
-        f32x2 carry0 = make_f32x2(r4.x, r4.y), carry1 = make_f32x2(r4.z, r4.w), dA0 = 0, dA1 = 0;
+        A0 = mul2(A0, both(kLog2e));
+        A1 = mul2(A1, both(kLog2e));
         // fold in the pieces behind, the last that the row has first
         if (pc.count > 1 && on)
 #pragma unroll 4
             for (int s = (len - 1) / pc.tokens; s > piece; --s) {
                 const f32x2 sum = both(pc.sums[((size_t)s * f.B + b) * f.D + c]);
-                const ulonglong2 v = *(const ulonglong2 *)(pc.slots + (size_t)s * f.B * f.D * N + at);
-                carry0 = fma2(decay2(sum, A0), carry0, v.x);
-                carry1 = fma2(decay2(sum, A1), carry1, v.y);
+                f32x2 v0, v1;
+                order.load(pc.slots + (size_t)s * f.B * f.D * N + at, v0, v1);
+                carry0 = fma2(decay2(sum, A0), carry0, v0);
+                carry1 = fma2(decay2(sum, A1), carry1, v1);
             }
         // the stored state ahead of the sub-tile that comes next
         const size_t pstride = (size_t)f.D * N;
         const float *point = parts.points + ((size_t)b * ((f.T + kSub - 1) / kSub) * f.D + c) * N + n0;
-        ulonglong2 state = make_ulonglong2(0, 0);
+        float2 state0 = make_float2(0.f, 0.f), state1 = state0;
         auto fetch_state = [&](int t) {
-            if (t >= t0 && t < t1 && on) state = *(const ulonglong2 *)(point + (size_t)(t / kSub) * pstride);
+            if (t >= t0 && t < t1 && on) {
+                state0 = *(const float2 *)(point + (size_t)(t / kSub) * pstride + order.first);
+                state1 = *(const float2 *)(point + (size_t)(t / kSub) * pstride + (order.first ^ 2));
+            }
         };
         fetch_state(t0 + tiles * kTile - kSub);
         __syncthreads();
@@ -151,20 +214,21 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
             for (int sub = kTile / kSub - 1; sub >= 0; --sub) {
                 const int tb = sub * kSub;
                 f32x2 a0[kSub], a1[kSub], h0[kSub + 1], h1[kSub + 1];
-                h0[0] = state.x;
-                h1[0] = state.y;
+                h0[0] = order.pair(state0);
+                h1[0] = order.pair(state1);
                 // A sub-tile behind the row's end has no stored state (it is 0 then); its tokens
                 // have delta = dc = 0 and change nothing.
                 fetch_state(tb0 + tb - kSub);
 #pragma unroll
                 for (int t = 0; t < kSub; ++t) {
                     const float2 du = *(const float2 *)(p + (tb + t) * S::CB * 2);
-                    const Quad<T> bq = *(const Quad<T> *)(sB + (tb + t) * N);
+                    f32x2 b0, b1;
+                    order.load(sB + (tb + t) * N, b0, b1);
                     const f32x2 d = both(du.x), u = both(du.y);
                     a0[t] = decay2(d, A0);
                     a1[t] = decay2(d, A1);
-                    h0[t + 1] = fma2(a0[t], h0[t], mul2(u, bq.lo()));
-                    h1[t + 1] = fma2(a1[t], h1[t], mul2(u, bq.hi()));
+                    h0[t + 1] = fma2(a0[t], h0[t], mul2(u, b0));
+                    h1[t + 1] = fma2(a1[t], h1[t], mul2(u, b1));
                 }
                 // A token's operands are loaded while the one before is in work, and its sums and
                 // stores wait until the next one's work is under way: loads stay behind stores, and
@@ -172,38 +236,32 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                 struct Token {
                     float2 du;
                     float dc;
-                    Quad<T> b, c;
+                    f32x2 b0, b1, c0, c1;
                 } now, next;
                 struct Sums {
-                    float v[8], su, sw, sy;
+                    f32x2 dB0, dB1, dC0, dC1;
+                    float su, sw, sy;
                 } done;
                 auto fetch = [&](Token &k, int t) {
                     k.du = *(const float2 *)(p + t * S::CB * 2);
                     k.dc = pd[t * S::CB];
-                    k.b = *(const Quad<T> *)(sB + t * N);
-                    k.c = *(const Quad<T> *)(sC + t * N);
+                    order.load(sB + t * N, k.b0, k.b1);
+                    order.load(sC + t * N, k.c0, k.c1);
                 };
-                auto store = [&](Sums &k, int t) {
-                    int which = 0;
-                    lane_sums<8, S::LN, 32>(k.v, lane, which);
+                auto store = [&](const Sums &k, int t) {
+                    store_sums<N, S::LN, S::CL>(k.dB0, k.dB1, k.dC0, k.dC1, lane, order, sq + t * kWarps * 2 * N);
                     *(float2 *)(o2 + t * kLanes * 2) = make_float2(k.su, k.sw);
                     if (f.z) o1[t * kLanes] = k.sy;
-                    constexpr int left = 8 / S::CL > 1 ? 8 / S::CL : 1;
-                    if (S::CL <= 8 || lane < 16) {
-                        float *o = sq + t * kWarps * 2 * N + (which >> 2) * N + (which & 3);
-#pragma unroll
-                        for (int j = 0; j < left; ++j) o[j] = k.v[j];
-                    }
                 };
                 fetch(now, tb + kSub - 1);
 #pragma unroll
                 for (int t = kSub - 1; t >= 0; --t) {
                     if (t > 0) fetch(next, tb + t - 1);
                     const f32x2 d = both(now.du.x), u = both(now.du.y), dc = both(now.dc);
-                    const f32x2 c0 = now.c.lo(), c1 = now.c.hi();
+                    const f32x2 c0 = now.c0, c1 = now.c1;
                     const f32x2 g0 = fma2(dc, c0, carry0), g1 = fma2(dc, c1, carry1);
                     const f32x2 dB0 = mul2(g0, u), dB1 = mul2(g1, u), dC0 = mul2(dc, h0[t + 1]), dC1 = mul2(dc, h1[t + 1]);
-                    const f32x2 pu = fma2(g1, now.b.hi(), mul2(g0, now.b.lo()));
+                    const f32x2 pu = fma2(g1, now.b1, mul2(g0, now.b0));
                     carry0 = mul2(a0[t], g0);
                     carry1 = mul2(a1[t], g1);
                     const f32x2 w0 = mul2(carry0, h0[t]), w1 = mul2(carry1, h1[t]);
@@ -212,8 +270,7 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                     dA1 = fma2(w1, d, dA1);
                     const f32x2 y = fma2(h1[t + 1], c1, mul2(h0[t + 1], c0));
                     if (t < kSub - 1) store(done, tb + t + 1);
-                    done = {{lo_f32(dB0), hi_f32(dB0), lo_f32(dB1), hi_f32(dB1), lo_f32(dC0), hi_f32(dC0), lo_f32(dC1),
-                             hi_f32(dC1)}, lo_f32(pu) + hi_f32(pu), lo_f32(pw) + hi_f32(pw), lo_f32(y) + hi_f32(y)};
+                    done = {dB0, dB1, dC0, dC1, lo_f32(pu) + hi_f32(pu), lo_f32(pw) + hi_f32(pw), lo_f32(y) + hi_f32(y)};
                     now = next;
                 }
                 store(done, tb);
@@ -221,8 +278,8 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
             __syncthreads();
         }
         if (on) {
-            *(ulonglong2 *)(parts.dA + (row_of_parts * f.D + c) * N + n0) = make_ulonglong2(dA0, dA1);
-            if (a.dh0 && piece == 0) *(ulonglong2 *)(a.dh0 + at) = make_ulonglong2(carry0, carry1);
+            order.store(parts.dA + (row_of_parts * f.D + c) * N + n0, dA0, dA1);
+            if (a.dh0 && piece == 0) order.store(a.dh0 + at, carry0, carry1);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHelperRegs));

@@ -112,8 +112,8 @@ def _type_of(x):
     return x.dtype
 
 
-def _new(shape, dtype, index, zero=False):
-    return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=index)
+def _new(shape, dtype, index):
+    return torch.empty(shape, dtype=dtype, device=index)
 
 
 def _workspace(ws, size, index):
@@ -188,8 +188,9 @@ def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, y, sta
         _dense(state, "state", (B, W - 1, D), index, dt)
     if lengths is not None:
         _dense(lengths, "lengths", (B,), index, _I32)
-    if y is None:
-        y = _new(shape, dt, index, lengths is not None)
+    zero_tail = y is None
+    if zero_tail:
+        y = _new(shape, dt, index)
     else:
         _dense(y, "y", shape, index, dt)
     if state_out is not None:
@@ -198,7 +199,7 @@ def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, y, sta
         state_out = _new((B, max(W - 1, 0), D), dt, index)
     status = lib().gdr_short_conv_fwd(
         x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths), y.data_ptr(), _ptr(state_out),
-        _conv_strides(x), B, H, T, d, W, act, _DTYPES[dt], handle)
+        _conv_strides(x), zero_tail, B, H, T, d, W, act, _DTYPES[dt], handle)
     if status:
         _check(status, "gdr_short_conv_fwd")
     return y, state_out
@@ -347,8 +348,9 @@ def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, 
         _dense(h0, "h0", (B, D, N), index)
     if lengths is not None:
         _dense(lengths, "lengths", (B,), index, _I32)
-    if y is None:
-        y = _new(shape, ty, index, lengths is not None)
+    zero_tail = y is None
+    if zero_tail:
+        y = _new(shape, ty, index)
     else:
         _dense(y, "y", shape, index, ty)
     if h_T is not None:
@@ -362,8 +364,8 @@ def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, 
                       *(z if z is not None else x).stride()[:2])
     status = L.gdr_ssm_scan_fwd(
         x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _ptr(D_skip), _ptr(z), _ptr(dt_bias),
-        _ptr(h0), _ptr(lengths), y.data_ptr(), _ptr(h_T), strides, B, T, D, G, N, 1 if dt_softplus else 0,
-        _DTYPES[ty], _ptr(ws), size, handle)
+        _ptr(h0), _ptr(lengths), y.data_ptr(), _ptr(h_T), strides, zero_tail, B, T, D, G, N,
+        1 if dt_softplus else 0, _DTYPES[ty], _ptr(ws), size, handle)
     if status:
         _check(status, "gdr_ssm_scan_fwd")
     return y, h_T

@@ -315,10 +315,12 @@ int gdr_chunk_fwd_noalloc(const void *q, const void *k, const void *v, const flo
  *                                   first; NULL = zeros
  *   lengths   [B]         int       tokens of each row, taken into [0,T]; NULL
  *                                   = T.  What lies behind a row's end is not
- *                                   read, and y is left as it was there
+ *                                   read
  *   y         [B,H,T,d]   dtype     output (written, dense)
  *   state_out [B,W-1,D]   dtype     the last W-1 rows of (state, x) (written);
  *                                   NULL = not wanted; may be `state` itself
+ *   zero_tail                       y behind a row's end: 0 = left as it was,
+ *                                   else set to zero
  * The convolution and scan calls need their dtype tensors aligned to one
  * element only, float and int vectors to 4 bytes; they take 16-byte (8-byte)
  * accesses where pointers and strides allow it, one element at a time
@@ -327,7 +329,7 @@ int gdr_chunk_fwd_noalloc(const void *q, const void *k, const void *v, const flo
 typedef enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
 
 int gdr_short_conv_fwd(const void *x, const float *weight, const float *bias, const void *state,
-                       const int *lengths, void *y, void *state_out, const long long *x_strides,
+                       const int *lengths, void *y, void *state_out, const long long *x_strides, int zero_tail,
                        int B, int H, int T, int d, int W, int act, int dtype, void *stream);
 
 /*
@@ -371,7 +373,7 @@ int gdr_short_conv_bwd(const void *x, const float *weight, const float *bias, co
  *   A        [D,N]       float     N in {8, 16, 32, 64}
  *   D_skip, dt_bias [D]  float     NULL = none
  *   h0       [B,D,N]     float     state before the sequence; NULL = zeros
- *   lengths  [B]         int       as gdr_short_conv_fwd
+ *   lengths  [B]         int       as gdr_short_conv_fwd, and zero_tail
  *   y        [B,T,D]     dtype     output (written, dense)
  *   h_T      [B,D,N]     float     state after each row's last token
  *                                  (written); NULL = not wanted; may be h0
@@ -386,7 +388,7 @@ size_t gdr_ssm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dt
 
 int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
                      const float *D_skip, const void *z, const float *dt_bias, const float *h0,
-                     const int *lengths, void *y, float *h_T, const long long *strides,
+                     const int *lengths, void *y, float *h_T, const long long *strides, int zero_tail,
                      int B, int T, int D, int G, int N, int dt_softplus, int dtype,
                      void *workspace, size_t ws_bytes, void *stream);
 

@@ -69,6 +69,9 @@ def test_forward(case):
     y, st = gdr.short_conv_fwd(d["x"], d["weight"], d["bias"], d["state"], "silu" if act else None, d["lengths"])
     near(y, y_ref, bound, dt, "y")
     np.testing.assert_array_equal(st.double().cpu().numpy(), st_ref)       # copies
+    if c["lengths"] is not None:      # a y made by the call is zero behind a row's end
+        for b, n in enumerate(c["lengths"].clamp(0, case[1]).tolist()):
+            assert not y[b, n:].any()
     # behind a row's end a given y stays as it is, and the state may be updated in place
     mine = torch.full_like(d["x"], 7.0).contiguous()
     if d["state"] is not None:

@@ -25,7 +25,7 @@ def longs(*v):
 def test_conv_arguments(L):
     def conv(x=GOOD, weight=GOOD, bias=None, state=None, lengths=None, y=GOOD, so=None, strides=None, B=1, H=1, T=4,
              d=8, W=4, act=1, dtype=1):
-        return L.gdr_short_conv_fwd(x, weight, bias, state, lengths, y, so, strides, B, H, T, d, W, act, dtype, None)
+        return L.gdr_short_conv_fwd(x, weight, bias, state, lengths, y, so, strides, 0, B, H, T, d, W, act, dtype, None)
     for bad in (dict(B=-1), dict(H=-1), dict(T=-1), dict(d=-1), dict(W=0), dict(act=2), dict(dtype=2), dict(x=None),
                 dict(weight=None), dict(y=None), dict(strides=longs(1, -1, 1))):
         assert conv(**bad) == INVALID, bad
@@ -69,7 +69,7 @@ def test_conv_bwd_arguments(L):
 def test_scan_arguments(L):
     def scan(x=GOOD, dt=GOOD, A=GOOD, Bm=GOOD, Cm=GOOD, skip=None, z=None, bias=None, h0=None, lengths=None, y=GOOD,
              hT=None, strides=None, B=1, T=4, D=8, G=1, N=16, dtype=1, ws=None, size=0):
-        return L.gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, skip, z, bias, h0, lengths, y, hT, strides, B, T, D, G, N, 1,
+        return L.gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, skip, z, bias, h0, lengths, y, hT, strides, 0, B, T, D, G, N, 1,
                                   dtype, ws, size, None)
     for bad in (dict(B=-1), dict(T=-1), dict(D=-1), dict(G=0), dict(N=0), dict(G=3), dict(dtype=2), dict(x=None),
                 dict(dt=None), dict(A=None), dict(Bm=None), dict(Cm=None), dict(y=None),

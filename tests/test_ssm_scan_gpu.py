@@ -85,7 +85,7 @@ def test_forward(case, softplus):
         T = case["T"]
         for b in range(case["B"]):
             n = T if c["lengths"] is None else int(c["lengths"][b].clamp(0, T))
-            assert torch.equal(mine[b, :n], y[b, :n]) and (mine[b, n:] == 7).all()
+            assert torch.equal(mine[b, :n], y[b, :n]) and (mine[b, n:] == 7).all() and not y[b, n:].any()
 
 
 def test_pieces_are_taken():
