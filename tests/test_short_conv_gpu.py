@@ -192,6 +192,23 @@ def test_other_stream_and_host_tensors():
     assert not y3.is_cuda and torch.equal(y.cpu(), y3) and torch.equal(st.cpu(), st3)
 
 
+def test_refusals():
+    c = make((2, 9, 16, 4, BF, True, True, True, None))
+    d = {k: cuda(v) for k, v in c.items()}
+    call = lambda **kw: gdr.short_conv_fwd(**{**d, **kw})   # noqa: E731
+    for bad, err in ((dict(weight=d["weight"].bfloat16()), TypeError), (dict(weight=d["weight"][:8]), ValueError),
+                     (dict(bias=d["bias"][:8]), ValueError), (dict(state=d["state"].float()), TypeError),
+                     (dict(state=d["state"][:, :2]), ValueError), (dict(activation="relu"), ValueError),
+                     (dict(lengths=torch.ones(2, dtype=torch.int64, device="cuda")), TypeError),
+                     (dict(lengths=torch.ones(3, dtype=torch.int32, device="cuda")), ValueError),
+                     (dict(weight=d["weight"].cpu()), ValueError), (dict(y=d["x"].transpose(0, 1)), ValueError),
+                     (dict(x=d["x"].half()), TypeError), (dict(x=d["x"][0]), ValueError),
+                     (dict(weight=None), ValueError),
+                     (dict(weight=torch.zeros(16, 5, device="cuda"), state=None), gdr.GDRError)):
+        with pytest.raises(err):
+            call(**bad)
+
+
 def test_graph_capture():
     c = make((2, 90, 64, 4, BF, True, True, True, None))
     d = {k: cuda(v) for k, v in c.items()}

@@ -193,6 +193,48 @@ def test_streams_host_and_repeats():
     assert not y2.is_cuda and torch.equal(y.cpu(), y2) and torch.equal(h.cpu(), h2)
 
 
+def test_stream_handles_workspaces_and_options():
+    c = make(1, 700, 40, 16)
+    d = {k: cuda(v) for k, v in c.items()}
+    y, h = gdr.ssm_scan_fwd(**d)
+    ws = torch.empty(gdr.ssm_scan_fwd_workspace_size(1, 700, 40, 1, 16) + 256, dtype=torch.uint8, device="cuda")
+    for kw in (dict(workspace=ws), dict(stream=torch.cuda.current_stream()), dict(stream=0),
+               dict(stream=torch.cuda.current_stream().cuda_stream)):
+        y2, h2 = gdr.ssm_scan_fwd(**d, **kw)
+        assert torch.equal(y, y2) and torch.equal(h, h2)
+    y2, none = gdr.ssm_scan_fwd(**d, final_state=False)
+    assert none is None and torch.equal(y, y2)
+    with pytest.raises(ValueError):
+        gdr.ssm_scan_fwd(**{**d, "dt": d["dt"][:, :-1]})
+    with pytest.raises(ValueError):
+        gdr.ssm_scan_fwd(**{**d, "x": d["x"].transpose(1, 2)})
+    with pytest.raises(ValueError):
+        gdr.ssm_scan_fwd(**{**d, "A": d["A"].cpu()})
+    with pytest.raises(TypeError):
+        gdr.ssm_scan_fwd(**{**d, "z": d["z"].float()})
+    with pytest.raises(TypeError):
+        gdr.ssm_scan_fwd(**{**d, "A": None})
+    with pytest.raises(gdr.GDRError):
+        gdr.ssm_scan_fwd(**{**d, "A": d["A"][:, :4].contiguous(), "Bm": d["Bm"][..., :4].contiguous(),
+                            "Cm": d["Cm"][..., :4].contiguous(), "h0": None})
+
+
+def test_rows_far_apart():
+    """Rows more than 2^31 elements apart (4.3 GB of address space, little of it touched)."""
+    B, T, D, N = 2, 40, 16, 8
+    c = make(B, T, D, N)
+    d = {k: cuda(v) for k, v in c.items()}
+    far = torch.empty(2 ** 31 + 16 + T * D, dtype=BF, device="cuda").as_strided((B, T, D), (2 ** 31 + 16, D, 1))
+    far.copy_(d["x"])
+    y, h = gdr.ssm_scan_fwd(**d)
+    y2, h2 = gdr.ssm_scan_fwd(**{**d, "x": far})
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    w = rnd(D, 4, seed=3).cuda()
+    assert torch.equal(gdr.short_conv_fwd(far, w)[0], gdr.short_conv_fwd(d["x"], w)[0])
+    g, g2 = gdr.short_conv_bwd(far, w, far), gdr.short_conv_bwd(d["x"], w, d["x"])
+    assert torch.equal(g[0], g2[0]) and torch.equal(g[1], g2[1])
+
+
 def test_graph_capture():
     c = make(1, 700, 40, 16)
     d = {k: cuda(v) for k, v in c.items()}
