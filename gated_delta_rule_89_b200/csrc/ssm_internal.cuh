@@ -341,13 +341,30 @@ __device__ __forceinline__ unsigned short load_if(const unsigned short *p, bool 
     return v;
 }
 
+// A read-only load that stays where it is written, ahead of the work that hides it.
+__device__ __forceinline__ float4 load_always(const float4 *p)
+{
+    float4 v;
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 load_always(const uint2 *p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
 // 4 consecutive elements, of which the first `valid` exist (the rest are 0).
-// VECTOR: groups are whole and aligned, so valid is <= 0 or >= 4.
-template <typename T, bool VECTOR>
+// VECTOR: groups are whole and aligned, so valid is <= 0 or >= 4.  ALL: they
+// all exist.
+template <typename T, bool VECTOR, bool ALL = false>
 __device__ __forceinline__ typename Pack<T, 4>::V load4(const T *p, int valid)
 {
     using V = typename Pack<T, 4>::V;
-    if constexpr (VECTOR) {
+    if constexpr (VECTOR && ALL) {
+        return load_always((const V *)p);
+    } else if constexpr (VECTOR) {
         return load_if((const V *)p, valid > 0);
     } else {
         using E = typename Pack<T, 1>::V;

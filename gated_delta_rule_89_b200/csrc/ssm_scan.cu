@@ -15,6 +15,8 @@
 // times what the same pipe would need for the tensors' bytes at HBM speed, so
 // the prompt form is bound by exponentials, not by HBM.  The rest of the work
 // is arranged to fit into the issue slots beside them.
+#include <type_traits>
+
 #include "ssm_internal.cuh"
 
 namespace gdr {
@@ -22,7 +24,7 @@ namespace {
 
 constexpr int kSms = 148;
 constexpr int kScanLanes = 128;            // threads of a block that run the recurrence
-constexpr int kTile = 32;                  // tokens between two block barriers
+constexpr int kUnit = 32;                  // pieces of a row are multiples of it
 
 // A block's share and its shared memory, for state size N and CPT channels a
 // scan thread (4 states of each).  With two channels the B and C that a thread
@@ -34,6 +36,9 @@ template <typename T, int N, int CPT> struct Shape {
     static constexpr int THREADS = kScanLanes + H;
     static constexpr int LPC = N / 4;                    // scan lanes of a channel
     static constexpr int CB = kScanLanes / LPC * CPT;    // channels of a block
+    // Tokens between two block barriers: 64 where two blocks still fit on an SM (at one block
+    // an SM, 1 x 4096 channels, 309 us against 408 with 32; at two 520 and 527).
+    static constexpr int kTile = CPT == 1 && N >= 16 && sizeof(T) == 2 ? 64 : 32;
     static constexpr int GR = CB / 4;                    // groups of 4 channels
     static constexpr int TPP = H / GR;                   // tokens the helpers cover at a time
     static constexpr int R = TPP >= kTile ? 1 : kTile / TPP;
@@ -73,11 +78,12 @@ struct Pieces {
 // and its sum of delta to sums[s].
 
 template <typename T, int N, int CPT, bool VECTOR, Mode MODE>
-__global__ void __launch_bounds__(Shape<T, N, CPT>::THREADS)
+__global__ void __launch_bounds__(Shape<T, N, CPT>::THREADS, 2)
 ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 {
     using S = Shape<T, N, CPT>;
     using V = typename Pack<T, 4>::V;
+    constexpr int kTile = S::kTile;
     extern __shared__ __align__(16) float sm[];
 
     const int per_row = blocks_per_group * a.G;
@@ -176,16 +182,15 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                     if (MODE == FULL) k[j].c = *(const Quad<T> *)(sc + at * N);
                 }
             };
-            fetch(now, 0);
-#pragma unroll
-            for (int t = 0; t < kTile; t += G) {
+            // four tokens from t on; `more`: four others follow
+            auto work = [&](int t, bool more) {
                 if (MODE == POINTS && t % kCheckpoint == 0 && t0 + i * kTile + t < t1) {
                     float *q = points + (size_t)(i * kTile + t) / kCheckpoint * a.D * N;
 #pragma unroll
                     for (int k = 0; k < CPT; ++k)
                         if (on[k]) *(ulonglong2 *)(q + k * N) = make_ulonglong2(h[k][0], h[k][1]);
                 }
-                if (t + G < kTile) fetch(next, t + G);
+                if (more) fetch(next, t + G);
                 float y[G][CPT];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
@@ -216,6 +221,15 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                         for (int k = 0; k < CPT; ++k) py[k][(t + j) * S::CB * S::LPC] = y[j][k];
                     now[j] = next[j];
                 }
+            };
+            fetch(now, 0);
+            const int count = t1 - t0 - i * kTile;
+            if (kBack || count >= kTile) {
+#pragma unroll
+                for (int t = 0; t < kTile; t += G) work(t, t + G < kTile);
+            } else {   // a row's last tile, as far as it has tokens (in fours: the rest change nothing)
+#pragma unroll 1
+                for (int t = 0; t < count; t += G) work(t, t + G < kTile);
             }
             __syncthreads();
         }
@@ -260,40 +274,51 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 
         V rx[S::R], rdt[S::R], rB[S::RB], rC[S::RB], ex[S::R], ez[S::R], rz[S::R];
         const T *pz = kBack ? pzo : nullptr;
-        auto fetch = [&](int i) {
-            const int tb = token_of(i);
-            const bool full = whole && tb + kTile <= t1;
+        // Tiles inside the piece load without predicates (which cost three instructions a load).
+        auto fetch_as = [&](int tb, auto inside) {
+            constexpr bool FULL_TILE = decltype(inside)::value;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
-                rx[r] = load4<T, VECTOR>(px + r * S::TPP * a.xs.t, valid);
-                rdt[r] = load4<T, VECTOR>(pdt + r * S::TPP * a.dts.t, valid);
-                if (kBack && pz) rz[r] = load4<T, VECTOR>(pz + r * S::TPP * a.zs.t, valid);
+                const int valid = FULL_TILE ? 4 : k < kTile && tb + k < t1 ? have : 0;
+                rx[r] = load4<T, VECTOR, FULL_TILE>(px + r * S::TPP * a.xs.t, valid);
+                rdt[r] = load4<T, VECTOR, FULL_TILE>(pdt + r * S::TPP * a.dts.t, valid);
+                if (kBack && pz) rz[r] = load4<T, VECTOR, FULL_TILE>(pz + r * S::TPP * a.zs.t, valid);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
-                const int valid = full && S::TPB <= kTile ? 4 : k < kTile && tb + k < t1 ? 4 : 0;
-                rB[r] = load4<T, VECTOR>(pB + r * S::TPB * a.bs.t, valid);
-                if (MODE == FULL) rC[r] = load4<T, VECTOR>(pC + r * S::TPB * a.cs.t, valid);
+                const int valid = FULL_TILE ? 4 : k < kTile && tb + k < t1 ? 4 : 0;
+                if (S::TPB > kTile && k >= kTile) continue;
+                rB[r] = load4<T, VECTOR, FULL_TILE>(pB + r * S::TPB * a.bs.t, valid);
+                if (MODE == FULL) rC[r] = load4<T, VECTOR, FULL_TILE>(pC + r * S::TPB * a.cs.t, valid);
             }
+        };
+        auto inside = [&](int tb) { return whole && tb + kTile <= t1 && S::TPP <= kTile; };
+        auto fetch = [&](int i) {
+            const int tb = token_of(i);
+            if (inside(tb)) fetch_as(tb, std::true_type{});
+            else fetch_as(tb, std::false_type{});
             px += kStep * a.xs.t;
             pdt += kStep * a.dts.t;
             pB += kStep * a.bs.t;
             if (MODE == FULL) pC += kStep * a.cs.t;
             if (kBack && pz) pz += kStep * a.zs.t;
         };
-        auto fetch_out = [&](int tile) {
-            const int tb = t0 + tile * kTile;
-            const bool full = whole && tb + kTile <= t1;
+        auto fetch_out_as = [&](int tb, auto inside) {
+            constexpr bool FULL_TILE = decltype(inside)::value;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
-                if (a.D_skip) ex[r] = load4<T, VECTOR>(pxo + r * S::TPP * a.xs.t, valid);
-                if (pzo) ez[r] = load4<T, VECTOR>(pzo + r * S::TPP * a.zs.t, valid);
+                const int valid = FULL_TILE ? 4 : k < kTile && tb + k < t1 ? have : 0;
+                if (a.D_skip) ex[r] = load4<T, VECTOR, FULL_TILE>(pxo + r * S::TPP * a.xs.t, valid);
+                if (pzo) ez[r] = load4<T, VECTOR, FULL_TILE>(pzo + r * S::TPP * a.zs.t, valid);
             }
+        };
+        auto fetch_out = [&](int tile) {
+            const int tb = t0 + tile * kTile;
+            if (inside(tb)) fetch_out_as(tb, std::true_type{});
+            else fetch_out_as(tb, std::false_type{});
             pxo += kTile * a.xs.t;
             if (pzo) pzo += kTile * a.zs.t;
         };
@@ -459,11 +484,11 @@ int blocks_per_group(int D, int G, int N, int cpt)
 }
 
 // One or two channels a thread, by how the blocks fill the SMs (two on each
-// either way).  Measured at N = 16 in us per 4096 tokens: one channel 264 for
-// a full set of 296 blocks and 204 for half of one, two channels 472 and 287;
-// so two are 11% faster where they fill the machine, and slower where half of
-// them would find no work (32-channel blocks against 64-channel ones: 2 x 4096
-// channels 527 and 574 us for 8192 tokens, 4 x 4096 channels 528 and 472 for 4096).
+// either way).  Measured at N = 16, bf16, in us per 4096 tokens: one channel
+// 260 for a full set of 296 blocks and 154 for half of one, two channels 467
+// and 287; so two are 10% faster where they fill the machine, and slower where
+// half of them would find no work (2 x 4096 channels: 260 and 287 us, 4 x 4096
+// channels: 527 and 467).
 int channels_per_thread(int B, int D, int G, int N)
 {
     const long long set = 2 * kSms, groups = (long long)B * G;
@@ -471,7 +496,7 @@ int channels_per_thread(int B, int D, int G, int N)
         const long long blocks = groups * blocks_per_group(D, G, N, cpt), rest = blocks % set;
         return blocks / set * full + (rest == 0 ? 0 : rest <= kSms ? half : full);
     };
-    return cost(2, 472, 287) < cost(1, 264, 204) ? 2 : 1;
+    return cost(2, 467, 287) < cost(1, 260, 154) ? 2 : 1;
 }
 
 // Few channels leave most of the machine idle; then a row is cut into pieces
@@ -483,10 +508,10 @@ Pieces plan(int B, int T, int D, int G, int N, void *workspace)
 {
     Pieces p = {1, T, nullptr, nullptr, nullptr};
     const long long blocks = (long long)B * G * blocks_per_group(D, G, N, channels_per_thread(B, D, G, N));
-    if (blocks > 0 && blocks * 2 <= kSms && T >= 8 * kTile) {
+    if (blocks > 0 && blocks * 2 <= kSms && T >= 8 * kUnit) {
         long long count = 2 * kSms / blocks;
-        if (count > T / (2 * kTile)) count = T / (2 * kTile);
-        p.tokens = (int)((T + count - 1) / count + kTile - 1) / kTile * kTile;
+        if (count > T / (2 * kUnit)) count = T / (2 * kUnit);
+        p.tokens = (int)((T + count - 1) / count + kUnit - 1) / kUnit * kUnit;
         p.count = (T + p.tokens - 1) / p.tokens;
     }
     if (p.count > 1) {
