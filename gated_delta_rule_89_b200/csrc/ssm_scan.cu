@@ -410,9 +410,10 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 // the step.  A thread owns 4 states of a channel in ROWS batch rows, so a
 // warp's accesses are whole lines, several loads are in flight, and A is read
 // once for the rows; each of a channel's lanes forms the time step and the
-// output of one row.
+// output of one row.  256 x 4096 channels, N = 16, bf16: 28.8 us, 143 MB at
+// 5.0 TB/s, with 4 rows and 5 blocks an SM; one row a thread took 39.
 template <typename T, int N, bool VECTOR>
-__global__ void __launch_bounds__(256) ssm_step_kernel(const ScanArgs a, int blocks_per_row)
+__global__ void __launch_bounds__(256, 5) ssm_step_kernel(const ScanArgs a, int blocks_per_row)
 {
     constexpr int LPC = N / 4, CB = 256 / LPC, ROWS = LPC < 4 ? LPC : 4;
     const int group = blockIdx.x / blocks_per_row, b0 = group * ROWS;
