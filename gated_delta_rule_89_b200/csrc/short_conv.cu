@@ -68,12 +68,28 @@ __device__ __forceinline__ void load_taps(const float *weight, const float *bias
     Lanes<VEC>::join(g, b);
 }
 
-// blockDim.x channel vectors by blockDim.y token runs; grid.x counts (batch,
-// run) pairs, grid.y channel vectors.
+// blockDim.x channel vectors by blockDim.y token runs.  Blocks are numbered
+// along the channels first, so that those at work together read whole token
+// rows (memory pages), not strips of far apart rows.
 struct ConvGrid {
-    dim3 block, grid;
-    int run, runs;   // tokens of a run, runs of a row
+    dim3 block;
+    int run, runs;        // tokens of a run, runs of a row
+    int across;           // blocks along the channels
+    long long down;       // blocks along the (batch, run) pairs
+    unsigned blocks() const { return (unsigned)(across * down); }
 };
+// This thread's channel vector and (batch, run) pair.
+struct ConvPlace {
+    int vector;
+    long long piece;
+    long long row;        // of the block
+};
+__device__ __forceinline__ ConvPlace conv_place(int across)
+{
+    const unsigned down = blockIdx.x / across;
+    return {(int)((blockIdx.x - down * across) * blockDim.x + threadIdx.x),
+            (long long)down * blockDim.y + threadIdx.y, down};
+}
 
 // The run length: long enough that the W-1 rows read again at its start (and,
 // backward, at its end) cost little, short enough that small problems still
@@ -92,7 +108,8 @@ ConvGrid conv_grid(int B, int T, long long vectors, int widest, int threads_per_
     g.run = (int)(run < 8 ? 8 : run > longest ? longest : run);
     g.runs = T > 0 ? (T + g.run - 1) / g.run : 1;
     const long long rows = (long long)B * g.runs;
-    g.grid = dim3((unsigned)((rows + g.block.y - 1) / g.block.y), (unsigned)((vectors + bx - 1) / bx));
+    g.across = (int)((vectors + bx - 1) / bx);
+    g.down = (rows + g.block.y - 1) / g.block.y;
     return g;
 }
 
@@ -100,14 +117,15 @@ ConvGrid conv_grid(int B, int T, long long vectors, int widest, int threads_per_
 // bf16 53 us (5.1 TB/s), against 71 with 16-byte vectors, eight rows and 4
 // blocks.  The two special-function operations of a sigmoid take 30 of them.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads, 8) conv_fwd_kernel(ConvArgs a, int run, int runs)
+__global__ void __launch_bounds__(kConvThreads, 8) conv_fwd_kernel(ConvArgs a, int run, int runs, int across)
 {
     using V = typename Pack<T, VEC>::V;
     // rows in work; as many more are on their way from memory meanwhile
     constexpr int U = VEC * sizeof(T) > 8 ? 2 : 4;
     const int D = a.H * a.d;
-    const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const ConvPlace at = conv_place(across);
+    const int c0 = at.vector * VEC;
+    const long long piece = at.piece;
     const int b = (int)(piece / runs);
     if (c0 >= D || b >= a.B) return;
     const int t0 = (int)(piece - (long long)b * runs) * run;
@@ -194,12 +212,12 @@ __global__ void __launch_bounds__(kConvThreads, 8) conv_fwd_kernel(ConvArgs a, i
 // and all of its rows' loads are in flight together.
 constexpr int kStepRows = 4;
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a)
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a, int across)
 {
     using V = typename Pack<T, VEC>::V;
     const int D = a.d;
-    const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    const int b0 = (blockIdx.x * blockDim.y + threadIdx.y) * kStepRows;
+    const ConvPlace at = conv_place(across);
+    const int c0 = at.vector * VEC, b0 = (int)at.piece * kStepRows;
     if (c0 >= D) return;
     V rows[kStepRows][W];
 #pragma unroll
@@ -252,13 +270,14 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a)
 // partial sums are added by a second kernel in a fixed order, so the result
 // does not depend on scheduling.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int run, int runs, float *part)
+__global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int run, int runs, int across, float *part)
 {
     using V = typename Pack<T, VEC>::V;
     constexpr int U = VEC == 1 ? 8 : sizeof(T) == 4 ? 2 : 4;   // as in the forward
     const int D = a.H * a.d;
-    const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    const long long piece = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const ConvPlace at = conv_place(across);
+    const int c0 = at.vector * VEC;
+    const long long piece = at.piece;
     const int b = (int)(piece / runs);
     using L = Lanes<VEC>;
     using P = typename L::P;
@@ -379,7 +398,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) sum[tid][v] += sum[tid + k * blockDim.x][v];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) part[((size_t)blockIdx.x * (W + 1) + j) * D + c0 + v] = sum[tid][v];
+            for (int v = 0; v < VEC; ++v) part[((size_t)at.row * (W + 1) + j) * D + c0 + v] = sum[tid][v];
         }
         __syncthreads();
     }
@@ -423,7 +442,7 @@ template <typename T, int VEC, int W>
 cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
 {
     const ConvGrid g = conv_grid(a.B, a.T, (long long)a.H * a.d / VEC, kConvThreads, 1024, 256);
-    conv_fwd_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a, g.run, g.runs);
+    conv_fwd_kernel<T, VEC, W><<<g.blocks(), g.block, 0, st>>>(a, g.run, g.runs, g.across);
     return cudaGetLastError();
 }
 
@@ -431,7 +450,7 @@ template <typename T, int VEC, int W>
 cudaError_t conv_step(const ConvArgs &a, cudaStream_t st)
 {
     const ConvGrid g = conv_grid((a.B + kStepRows - 1) / kStepRows, 1, a.d / VEC, kConvThreads, 512, 8);
-    conv_step_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a);
+    conv_step_kernel<T, VEC, W><<<g.blocks(), g.block, 0, st>>>(a, g.across);
     return cudaGetLastError();
 }
 
@@ -443,10 +462,10 @@ cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
 {
     const int D = a.H * a.d;
     const ConvGrid g = conv_bwd_grid(a.B, a.T, D / VEC);
-    conv_bwd_kernel<T, VEC, W><<<g.grid, g.block, 0, st>>>(a, g.run, g.runs, (float *)a.workspace);
+    conv_bwd_kernel<T, VEC, W><<<g.blocks(), g.block, 0, st>>>(a, g.run, g.runs, g.across, (float *)a.workspace);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    conv_bwd_sum_kernel<<<((W + 1) * D + 31) / 32, dim3(32, 32), 0, st>>>((const float *)a.workspace, (int)g.grid.x,
+    conv_bwd_sum_kernel<<<((W + 1) * D + 31) / 32, dim3(32, 32), 0, st>>>((const float *)a.workspace, (int)g.down,
                                                                             D, W, a.dweight, a.dbias);
     return cudaGetLastError();
 }
@@ -510,7 +529,7 @@ size_t short_conv_bwd_workspace_bytes(int B, int H, int T, int d, int W)
 {
     // the partial sums of whichever access width the call will take
     const long long D = (long long)H * d;
-    const unsigned wide = d % 4 == 0 ? conv_bwd_grid(B, T, D / 4).grid.x : 0, narrow = conv_bwd_grid(B, T, D).grid.x;
+    const long long wide = d % 4 == 0 ? conv_bwd_grid(B, T, D / 4).down : 0, narrow = conv_bwd_grid(B, T, D).down;
     return (size_t)(wide > narrow ? wide : narrow) * (size_t)(W + 1) * (size_t)D * sizeof(float);
 }
 
