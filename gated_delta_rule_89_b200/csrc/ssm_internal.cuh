@@ -3,6 +3,8 @@
 // launchers, and the scalar functions both use.
 #pragma once
 
+#include <atomic>
+
 #include "gdr_internal.cuh"
 
 namespace gdr {
@@ -407,6 +409,21 @@ template <> struct Quad<__nv_bfloat16> {
     __device__ __forceinline__ f32x2 lo() const { return make_f32x2(bf16_lo(v.x), bf16_hi(v.x)); }
     __device__ __forceinline__ f32x2 hi() const { return make_f32x2(bf16_lo(v.y), bf16_hi(v.y)); }
 };
+
+// Lets `kernel` have `bytes` of shared memory; `done` (one for each kernel)
+// holds the devices where that has been said.
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<unsigned long long> &done)
+{
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 inline bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 

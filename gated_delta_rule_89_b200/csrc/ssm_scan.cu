@@ -541,7 +541,8 @@ cudaError_t run_scan(const ScanArgs &a, const Pieces &p, int pieces, cudaStream_
 {
     using S = Shape<T, N, CPT>;
     auto k = ssm_scan_kernel<T, N, CPT, VECTOR, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_shared(k, S::smem, done);
     if (e != cudaSuccess) return e;
     const int bpg = blocks_per_group(a.D, a.G, N, CPT);
     k<<<dim3((unsigned)((long long)a.B * a.G * bpg), pieces), S::THREADS, S::smem, st>>>(a, p, bpg);

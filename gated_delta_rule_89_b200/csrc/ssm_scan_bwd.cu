@@ -23,6 +23,8 @@
 // with the helpers too.  Blocks' parts of dB and dC, and batch rows' parts of
 // dA, dD and ddt_bias, are added by a last kernel in a fixed order: no atomics,
 // equal calls give equal bits.
+#include <type_traits>
+
 #include "ssm_internal.cuh"
 
 namespace gdr {
@@ -313,25 +315,31 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
             V x[S::R];
             float slope[S::R][4], dz[S::R][4];
         } old, mid;
-        auto fetch = [&](int i) {
-            const int tb = token_of(i);
-            const bool full = whole && tb + kTile <= t1;
+        // tiles inside the piece load without predicates
+        auto fetch_as = [&](int tb, auto inside) {
+            constexpr bool FULL_TILE = decltype(inside)::value;
 #pragma unroll
             for (int r = 0; r < S::R; ++r) {
                 const int k = tok + r * S::TPP;
-                const int valid = full && S::TPP <= kTile ? 4 : k < kTile && tb + k < t1 ? have : 0;
-                rx[r] = load4<T, VECTOR>(px + r * S::TPP * f.xs.t, valid);
-                rdt[r] = load4<T, VECTOR>(pdt + r * S::TPP * f.dts.t, valid);
-                rdy[r] = load4<T, VECTOR>(pdy + r * S::TPP * a.dys.t, valid);
-                if (pz) rz[r] = load4<T, VECTOR>(pz + r * S::TPP * f.zs.t, valid);
+                const int valid = FULL_TILE ? 4 : k < kTile && tb + k < t1 ? have : 0;
+                rx[r] = load4<T, VECTOR, FULL_TILE>(px + r * S::TPP * f.xs.t, valid);
+                rdt[r] = load4<T, VECTOR, FULL_TILE>(pdt + r * S::TPP * f.dts.t, valid);
+                rdy[r] = load4<T, VECTOR, FULL_TILE>(pdy + r * S::TPP * a.dys.t, valid);
+                if (pz) rz[r] = load4<T, VECTOR, FULL_TILE>(pz + r * S::TPP * f.zs.t, valid);
             }
 #pragma unroll
             for (int r = 0; r < S::RB; ++r) {
                 const int k = tokb + r * S::TPB;
-                const int valid = full && S::TPB <= kTile ? 4 : k < kTile && tb + k < t1 ? 4 : 0;
-                rB[r] = load4<T, VECTOR>(pB + r * S::TPB * f.bs.t, valid);
-                rC[r] = load4<T, VECTOR>(pC + r * S::TPB * f.cs.t, valid);
+                const int valid = FULL_TILE ? 4 : k < kTile && tb + k < t1 ? 4 : 0;
+                if (S::TPB > kTile && k >= kTile) continue;
+                rB[r] = load4<T, VECTOR, FULL_TILE>(pB + r * S::TPB * f.bs.t, valid);
+                rC[r] = load4<T, VECTOR, FULL_TILE>(pC + r * S::TPB * f.cs.t, valid);
             }
+        };
+        auto fetch = [&](int i) {
+            const int tb = token_of(i);
+            if (whole && tb + kTile <= t1 && S::TPP <= kTile) fetch_as(tb, std::true_type{});
+            else fetch_as(tb, std::false_type{});
             px -= kTile * f.xs.t;
             pdt -= kTile * f.dts.t;
             pdy -= kTile * a.dys.t;
@@ -624,7 +632,8 @@ cudaError_t run_bwd(const ScanBwdArgs &a, const BwdParts &p, cudaStream_t st)
 {
     using S = Shape<T, N>;
     auto k = ssm_bwd_kernel<T, N, VECTOR>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_shared(k, S::smem, done);
     if (e != cudaSuccess) return e;
     const int bpg = blocks_per_group(a.f.D, a.f.G, N);
     k<<<dim3((unsigned)((long long)a.f.B * a.f.G * bpg), p.pc.count), kThreads, S::smem, st>>>(a, p, bpg);

@@ -33,19 +33,25 @@ _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _run(call, x, stream, args):
+def _here(x, stream):
+    """x's device if that is the current one and the call runs on its current stream, else None:
+    the case in which nothing has to be switched or copied."""
+    try:
+        index = x.get_device()
+    except AttributeError:
+        raise TypeError("x must be a tensor") from None
+    return index if stream is None and index >= 0 and index == _current_device() else None
+
+
+def _elsewhere(call, x, stream, *args):
     """call(stream handle, device index, x, *args) with the device and the stream current that it
     runs on, so that what it allocates belongs to that stream.  A host x: every tensor is copied
     to the current device first and the results back afterwards."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a tensor")
     index = x.get_device()
     host = index < 0
     if host:
         _type_of(x)
         index = torch.cuda.current_device()
-    elif stream is None and index == _current_device():
-        return call(_current_stream(index), index, x, *args)
     dev = torch.device("cuda", index)
     if stream is None:
         with torch.cuda.device(dev):
@@ -175,7 +181,11 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     activation "silu" or None; lengths int32 [B].  Returns (y, contiguous in x's shape and
     type, and the state after the prompt or None); ``state_out`` may be ``state``.
     """
-    return _run(_conv_fwd, x, stream, (weight, bias, state, activation, lengths, y, state_out, final_state))
+    index = _here(x, stream)
+    if index is None:
+        return _elsewhere(_conv_fwd, x, stream, weight, bias, state, activation, lengths, y, state_out, final_state)
+    return _conv_fwd(_current_stream(index), index, x, weight, bias, state, activation, lengths, y, state_out,
+                     final_state)
 
 
 def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, y, state_out, final_state):
@@ -213,9 +223,12 @@ def short_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, 
     x [B,D] (rows may be strided); state [B,W-1,D] in x's type is shifted IN PLACE; weight, bias
     and activation as ``short_conv_fwd``.  Returns y [B,D].
     """
-    if isinstance(x, torch.Tensor) and x.get_device() < 0:
-        raise ValueError("short_conv_step works on CUDA tensors: the state is updated in place")
-    return _run(_conv_step, x, stream, (state, weight, bias, activation, y))
+    index = _here(x, stream)
+    if index is None:
+        if x.get_device() < 0:
+            raise ValueError("short_conv_step works on CUDA tensors: the state is updated in place")
+        return _elsewhere(_conv_step, x, stream, state, weight, bias, activation, y)
+    return _conv_step(_current_stream(index), index, x, state, weight, bias, activation, y)
 
 
 def _conv_step(handle, index, x, state, weight, bias, activation, y):
@@ -255,7 +268,11 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias
     state).  dx has x's shape and its order in memory (token rows stay token rows); it is
     zero behind a row's end.
     """
-    return _run(_conv_bwd, x, stream, (weight, dy, bias, state, dstate_out, activation, lengths, workspace))
+    index = _here(x, stream)
+    if index is None:
+        return _elsewhere(_conv_bwd, x, stream, weight, dy, bias, state, dstate_out, activation, lengths, workspace)
+    return _conv_bwd(_current_stream(index), index, x, weight, dy, bias, state, dstate_out, activation, lengths,
+                     workspace)
 
 
 def _conv_bwd(handle, index, x, weight, dy, bias, state, dstate_out, activation, lengths, workspace):
@@ -295,7 +312,8 @@ def _conv_bwd(handle, index, x, weight, dy, bias, state, dstate_out, activation,
 def _scan_inputs(index, x, dt, A, Bm, Cm, D_skip, z, dt_bias):
     """Checks what the three scan calls share; returns (G, N)."""
     ty, shape = _type_of(x), x.shape
-    _rows(x, "x", shape, index, ty)
+    if not x.is_contiguous():
+        _rows(x, "x", shape, index, ty)
     _rows(dt, "dt", shape, index, ty)
     if z is not None:
         _rows(z, "z", shape, index, ty)
@@ -333,8 +351,12 @@ def ssm_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     A [D,N], D_skip [D], dt_bias [D], h0 [B,D,N] fp32; N in 8, 16, 32, 64; lengths int32 [B].
     Returns (y [B,T,D] in x's type, h_T [B,D,N] fp32 or None); ``h_T`` may be ``h0``.
     """
-    return _run(_scan_fwd, x, stream, (dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T,
-                final_state, workspace))
+    index = _here(x, stream)
+    if index is None:
+        return _elsewhere(_scan_fwd, x, stream, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T,
+                          final_state, workspace)
+    return _scan_fwd(_current_stream(index), index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y,
+                     h_T, final_state, workspace)
 
 
 def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T, final_state,
@@ -380,9 +402,12 @@ def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.
     x, dt, z [B,D] and Bm, Cm [B,G,N] (rows may be strided), the rest as ``ssm_scan_fwd``.
     Returns y [B,D].
     """
-    if isinstance(x, torch.Tensor) and x.get_device() < 0:
-        raise ValueError("ssm_scan_step works on CUDA tensors: the state is updated in place")
-    return _run(_scan_step, x, stream, (dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y))
+    index = _here(x, stream)
+    if index is None:
+        if x.get_device() < 0:
+            raise ValueError("ssm_scan_step works on CUDA tensors: the state is updated in place")
+        return _elsewhere(_scan_step, x, stream, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y)
+    return _scan_step(_current_stream(index), index, x, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y)
 
 
 def _scan_step(handle, index, x, dt, A, Bm, Cm, h, D_skip, z, dt_bias, dt_softplus, y):
@@ -421,7 +446,12 @@ def ssm_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0), each in its input's shape and type
     (contiguous) and None where that input is; dx, ddt, dB, dC and dz are zero behind a row's end.
     """
-    return _run(_scan_bwd, x, stream, (dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace))
+    index = _here(x, stream)
+    if index is None:
+        return _elsewhere(_scan_bwd, x, stream, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths,
+                          workspace)
+    return _scan_bwd(_current_stream(index), index, x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T,
+                     lengths, workspace)
 
 
 def _scan_bwd(handle, index, x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softplus, h0, dh_T, lengths, workspace):
