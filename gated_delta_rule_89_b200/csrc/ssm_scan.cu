@@ -26,19 +26,28 @@ constexpr int kSms = 148;
 constexpr int kScanLanes = 128;            // threads of a block that run the recurrence
 constexpr int kUnit = 32;                  // pieces of a row are multiples of it
 
+enum Mode {
+    FULL,    // the outputs and the final state
+    LOCAL,   // the state that a piece of a row ends with when it starts from zero
+    POINTS,  // the states ahead of every kCheckpoint-th token, for the backward
+    ADJOINT  // the gradient of the state ahead of a piece when that behind it is zero: a walk back
+             // with dy silu(z) in the place of u and C in the place of B
+};
+
 // A block's share and its shared memory, for state size N and CPT channels a
 // scan thread (4 states of each).  With two channels the B and C that a thread
 // loads serve twice, which matters: shared memory returns 128 bytes a clock,
 // and with one channel the loads of a token take 40 clocks of an SM against 32
 // for its exponentials.  With one channel there are twice as many blocks.
-template <typename T, int N, int CPT> struct Shape {
+template <typename T, int N, int CPT, Mode MODE> struct Shape {
     static constexpr int H = CPT == 1 && N > 16 ? kScanLanes : 2 * kScanLanes;   // helper threads
     static constexpr int THREADS = kScanLanes + H;
     static constexpr int LPC = N / 4;                    // scan lanes of a channel
     static constexpr int CB = kScanLanes / LPC * CPT;    // channels of a block
     // Tokens between two block barriers: 64 where two blocks still fit on an SM (at one block
-    // an SM, 1 x 4096 channels, 309 us against 408 with 32; at two 520 and 527).
-    static constexpr int kTile = CPT == 1 && N >= 16 && sizeof(T) == 2 ? 64 : 32;
+    // an SM, 1 x 4096 channels, 309 us against 408 with 32; at two 520 and 527); the passes
+    // without outputs have less to do between the barriers and are 2% to 4% faster with 32.
+    static constexpr int kTile = MODE == FULL && CPT == 1 && N >= 16 && sizeof(T) == 2 ? 64 : 32;
     static constexpr int GR = CB / 4;                    // groups of 4 channels
     static constexpr int TPP = H / GR;                   // tokens the helpers cover at a time
     static constexpr int R = TPP >= kTile ? 1 : kTile / TPP;
@@ -57,14 +66,6 @@ template <typename T, int N, int CPT> struct Shape {
 // folded in, both meet 8 different banks.
 __device__ __forceinline__ int swz(int chunk) { return chunk ^ ((chunk >> 3) & 7); }
 
-enum Mode {
-    FULL,    // the outputs and the final state
-    LOCAL,   // the state that a piece of a row ends with when it starts from zero
-    POINTS,  // the states ahead of every kCheckpoint-th token, for the backward
-    ADJOINT  // the gradient of the state ahead of a piece when that behind it is zero: a walk back
-             // with dy silu(z) in the place of u and C in the place of B
-};
-
 // pieces of a row (time is split when there are few channels), tokens of a
 // piece, and the piece states: slot [s][B][D][N] is what piece s starts from
 // (slot 0: h0) before the pieces ahead of it are folded in, and
@@ -78,10 +79,10 @@ struct Pieces {
 // and its sum of delta to sums[s].
 
 template <typename T, int N, int CPT, bool VECTOR, Mode MODE>
-__global__ void __launch_bounds__(Shape<T, N, CPT>::THREADS, 2)
+__global__ void __launch_bounds__(Shape<T, N, CPT, MODE>::THREADS, 2)
 ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
 {
-    using S = Shape<T, N, CPT>;
+    using S = Shape<T, N, CPT, MODE>;
     using V = typename Pack<T, 4>::V;
     constexpr int kTile = S::kTile;
     extern __shared__ __align__(16) float sm[];
@@ -539,7 +540,7 @@ template <typename T> bool scan_vectors(const ScanArgs &a)
 template <typename T, int N, int CPT, bool VECTOR, Mode MODE>
 cudaError_t run_scan(const ScanArgs &a, const Pieces &p, int pieces, cudaStream_t st)
 {
-    using S = Shape<T, N, CPT>;
+    using S = Shape<T, N, CPT, MODE>;
     auto k = ssm_scan_kernel<T, N, CPT, VECTOR, MODE>;
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = allow_shared(k, S::smem, done);
