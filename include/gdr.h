@@ -347,7 +347,7 @@ int gdr_short_conv_step(const void *x, const float *weight, const float *bias, v
  * row's end, where dy is not read.  dstate_out NULL = zeros; dbias and dstate
  * NULL = not wanted.  dweight and dbias are summed in fp32 in a fixed order:
  * equal calls give equal bits.  The workspace (device, 16-byte aligned) holds
- * the partial sums.
+ * the partial sums; calls that may overlap need their own.
  */
 size_t gdr_short_conv_bwd_workspace_size(int B, int H, int T, int d, int W, int dtype);
 
@@ -382,7 +382,8 @@ int gdr_short_conv_bwd(const void *x, const float *weight, const float *bias, co
  *                                  0; the rest is dense); NULL = all dense
  * A, h0, h_T and the workspace must be 16-byte aligned.  The workspace (0
  * bytes for most sizes) holds the states between the pieces that a row is cut
- * into when there are few channels.
+ * into when there are few channels.  Calls that may overlap, captured graphs
+ * among them, need workspaces of their own.
  */
 size_t gdr_ssm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dtype);
 
