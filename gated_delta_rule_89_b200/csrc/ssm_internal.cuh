@@ -292,7 +292,6 @@ __device__ __forceinline__ void pack(unsigned short &v, const float *f) { v = (u
 template <typename V> __device__ __forceinline__ V zero_pack();
 template <> __device__ __forceinline__ float4 zero_pack<float4>() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 template <> __device__ __forceinline__ uint2 zero_pack<uint2>() { return make_uint2(0u, 0u); }
-template <> __device__ __forceinline__ uint4 zero_pack<uint4>() { return make_uint4(0u, 0u, 0u, 0u); }
 template <> __device__ __forceinline__ float zero_pack<float>() { return 0.f; }
 template <> __device__ __forceinline__ unsigned short zero_pack<unsigned short>() { return 0; }
 
@@ -310,14 +309,6 @@ __device__ __forceinline__ float4 load_if(const float4 *p, bool on)
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
         "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w) : "l"(p), "r"((int)on));
-    return v;
-}
-__device__ __forceinline__ uint4 load_if(const uint4 *p, bool on)
-{
-    uint4 v;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
-        "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((int)on));
     return v;
 }
 __device__ __forceinline__ uint2 load_if(const uint2 *p, bool on)

@@ -10,11 +10,18 @@
 // Mixer I", section "Mamba2: Linear Attention with Decay", with a decay of
 // its own for every channel and state and no delta term).
 //
-// Every (token, channel, state) costs one exponential, and the special
-// function pipe gives 16 of them per clock and SM: with N = 16 that is 12
-// times what the same pipe would need for the tensors' bytes at HBM speed, so
-// the prompt form is bound by exponentials, not by HBM.  The rest of the work
-// is arranged to fit into the issue slots beside them.
+// Every (token, channel, state) costs one exponential, and every (token,
+// channel) three more special functions for the time step and the gate.  The
+// pipe gives 16 of them per clock and SM: at N = 16 that is 3.3 times as long
+// as the tensors' bytes take at HBM speed, so the prompt form is bound by
+// exponentials, and after them by issue slots.  2 x 8192 x 4096 channels, bf16:
+// 520 us, where the exponentials alone need 274 (and the 256 blocks keep 86%
+// of the SMs busy).
+//
+// A block's first four warps run the recurrence, one channel (or two) and 4
+// states a thread; the others, one tile ahead and behind, load, form delta and
+// delta x, add the partial sums of C h, and write the outputs.  The two meet at
+// one barrier a tile, in double-buffered shared memory.
 #include <type_traits>
 
 #include "ssm_internal.cuh"
@@ -36,9 +43,9 @@ enum Mode {
 
 // A block's share and its shared memory, for state size N and CPT channels a
 // scan thread (4 states of each).  With two channels the B and C that a thread
-// loads serve twice, which matters: shared memory returns 128 bytes a clock,
-// and with one channel the loads of a token take 40 clocks of an SM against 32
-// for its exponentials.  With one channel there are twice as many blocks.
+// loads serve twice: shared memory returns 128 bytes a clock, and one channel's
+// loads of a token take 24 (bf16) or 40 (fp32) clocks of an SM against 32 for
+// its exponentials.  With one channel there are twice as many blocks.
 template <typename T, int N, int CPT, Mode MODE> struct Shape {
     static constexpr int H = CPT == 1 && N > 16 ? kScanLanes : 2 * kScanLanes;   // helper threads
     static constexpr int THREADS = kScanLanes + H;
