@@ -11,6 +11,10 @@ the formulas).  Differences in manner:
   are not read and ``y`` is left as it is; a ``y`` made by the call is zero
   there.
 * Outputs and workspaces are made on the stream that the call runs on.
+* With a host ``x`` the inputs are copied to the current device and the results
+  come back as new host tensors; an output that the caller gives has to lie on
+  the device (a host one is refused), and the step calls, which update a state
+  in place, take device tensors only.
 """
 from __future__ import annotations
 
@@ -43,14 +47,19 @@ def _here(x, stream):
     return index if stream is None and index >= 0 and index == _current_device() else None
 
 
-def _elsewhere(call, x, stream, *args):
-    """call(stream handle, device index, x, *args) with the device and the stream current that it
-    runs on, so that what it allocates belongs to that stream.  A host x: every tensor is copied
-    to the current device first and the results back afterwards."""
+def _elsewhere(call, x, stream, *args, outputs=()):
+    """call(stream handle, device index, x, *args, *outputs) with the device and the stream current
+    that it runs on, so that what it allocates belongs to that stream.  A host x: every tensor of
+    `args` is copied to the current device first and the results back afterwards.  `outputs` (name
+    and tensor or None) are not copied, as the call would write the copies: they have to lie on the
+    device."""
     index = x.get_device()
     host = index < 0
     if host:
         _type_of(x)
+        for name, t in outputs:
+            if isinstance(t, torch.Tensor) and t.get_device() < 0:
+                raise ValueError(f"{name} is a host tensor: a call with host inputs returns its results in new ones")
         index = torch.cuda.current_device()
     dev = torch.device("cuda", index)
     if stream is None:
@@ -64,7 +73,7 @@ def _elsewhere(call, x, stream, *args):
         if host:
             x = _to_device(x, dev)
             args = [_to_device(t, dev) if isinstance(t, torch.Tensor) else t for t in args]
-        out = call(stream.cuda_stream, index, x, *args)
+        out = call(stream.cuda_stream, index, x, *args, **dict(outputs))
         return tuple(_to_host(t) for t in out) if host else out
 
 
@@ -183,12 +192,13 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     """
     index = _here(x, stream)
     if index is None:
-        return _elsewhere(_conv_fwd, x, stream, weight, bias, state, activation, lengths, y, state_out, final_state)
-    return _conv_fwd(_current_stream(index), index, x, weight, bias, state, activation, lengths, y, state_out,
-                     final_state)
+        return _elsewhere(_conv_fwd, x, stream, weight, bias, state, activation, lengths, final_state,
+                          outputs=(("y", y), ("state_out", state_out)))
+    return _conv_fwd(_current_stream(index), index, x, weight, bias, state, activation, lengths, final_state, y,
+                     state_out)
 
 
-def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, y, state_out, final_state):
+def _conv_fwd(handle, index, x, weight, bias, state, activation, lengths, final_state, y, state_out):
     dt = _type_of(x)
     B, H, T, d = _conv_shape(x)
     shape, D = x.shape, H * d
@@ -353,14 +363,14 @@ def ssm_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.T
     """
     index = _here(x, stream)
     if index is None:
-        return _elsewhere(_scan_fwd, x, stream, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T,
-                          final_state, workspace)
-    return _scan_fwd(_current_stream(index), index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y,
-                     h_T, final_state, workspace)
+        return _elsewhere(_scan_fwd, x, stream, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths,
+                          final_state, workspace, outputs=(("y", y), ("h_T", h_T)))
+    return _scan_fwd(_current_stream(index), index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths,
+                     final_state, workspace, y, h_T)
 
 
-def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, y, h_T, final_state,
-              workspace):
+def _scan_fwd(handle, index, x, dt, A, Bm, Cm, D_skip, z, dt_bias, dt_softplus, h0, lengths, final_state, workspace,
+              y, h_T):
     if x.dim() != 3:
         raise ValueError("x must be [B,T,D]")
     shape, ty = x.shape, x.dtype

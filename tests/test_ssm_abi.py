@@ -130,3 +130,16 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         gdr.ssm_scan_step(x[:, 0], x[:, 0], torch.zeros(8, 16), torch.zeros(2, 1, 16), torch.zeros(2, 1, 16),
                           torch.zeros(2, 8, 16))
+
+
+def test_binding_refuses_host_outputs():
+    """A host call's results are new tensors: an output that would stay unwritten is refused (before
+    any CUDA call is made)."""
+    x, w, st = torch.zeros(2, 4, 8), torch.zeros(8, 4), torch.zeros(2, 3, 8)
+    for kw in (dict(y=torch.zeros(2, 4, 8)), dict(state_out=st), dict(state_out=torch.zeros(2, 3, 8))):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            gdr.short_conv_fwd(x, w, state=st, **kw)
+    h, bc = torch.zeros(2, 8, 16), torch.zeros(2, 4, 1, 16)
+    for kw in (dict(y=torch.zeros(2, 4, 8)), dict(h_T=h), dict(h_T=torch.zeros(2, 8, 16))):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            gdr.ssm_scan_fwd(x, x, torch.zeros(8, 16), bc, bc, h0=h, **kw)
