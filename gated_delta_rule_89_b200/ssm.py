@@ -31,10 +31,21 @@ _I64x3 = ctypes.c_longlong * 3
 _I64x5 = ctypes.c_longlong * 5
 _I64x10 = ctypes.c_longlong * 10
 _I64x12 = ctypes.c_longlong * 12
+
 # A decode step takes a few microseconds on the device, so the host's share counts: these two are
 # what torch.cuda.current_device() and current_stream() come to, without the objects around them.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# They are looked up by the first call: a build of torch without CUDA does not have them, and can
+# still import this package (and build the library).
+def _current_device():
+    global _current_device
+    _current_device = torch._C._cuda_getDevice
+    return _current_device()
+
+
+def _current_stream(index):
+    global _current_stream
+    _current_stream = torch._C._cuda_getCurrentRawStream
+    return _current_stream(index)
 
 
 def _here(x, stream):

@@ -1,5 +1,8 @@
 """The convolution's and the scan's entry points refuse bad arguments on the host (no GPU needed)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -143,3 +146,15 @@ def test_binding_refuses_host_outputs():
     for kw in (dict(y=torch.zeros(2, 4, 8)), dict(h_T=h), dict(h_T=torch.zeros(2, 8, 16))):
         with pytest.raises(ValueError, match=next(iter(kw))):
             gdr.ssm_scan_fwd(x, x, torch.zeros(8, 16), bc, bc, h0=h, **kw)
+
+
+def test_import_without_cuda_in_torch():
+    """A torch build without CUDA has no raw device and stream queries; the package and its build
+    module still import there."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import gated_delta_rule_89_b200, gated_delta_rule_89_b200.build\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(gdr.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
