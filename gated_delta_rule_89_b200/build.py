@@ -50,7 +50,9 @@ def needs_build() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
-    os.makedirs(OBJ, exist_ok=True)
+    # objects made with other flags lie in a folder of their own: no later build links them
+    objdir = os.path.join(OBJ, "extra") if extra else OBJ
+    os.makedirs(objdir, exist_ok=True)
     headers = [p for p in deps() if not p.endswith(".cu")] + [os.path.abspath(__file__)]
 
     def run(cmd):
@@ -59,7 +61,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         subprocess.run(cmd, check=True)
 
     def compile_one(src):
-        obj = os.path.join(OBJ, os.path.basename(src) + ".o")
+        obj = os.path.join(objdir, os.path.basename(src) + ".o")
         if not force and not extra and os.path.exists(obj) and \
                 all(os.path.getmtime(obj) >= os.path.getmtime(p) for p in [src, *headers]):
             return obj
