@@ -10,10 +10,19 @@ If the library has not been built, importing the functions raises.
 Host tensors are accepted too: they are copied to the current CUDA device,
 processed, and the outputs are copied back to host memory (this is what the
 end-to-end measurement times).
+
+``stream`` (a ``torch.cuda.Stream`` or a raw handle) lets a call run on another
+stream than the current one.  The call then allocates and copies on that stream
+and waits for no other: the caller orders the two streams.  The allocator keeps
+the memory of the tensors given and returned until both streams are past their
+use; of a raw handle it knows nothing, so what a call on one is given has to live
+until that stream is done.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import Optional, Tuple
 
@@ -129,6 +138,46 @@ def _stream_handle(device: torch.device, stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(h)
 
 
+def _stream_on(stream, dev: torch.device) -> torch.cuda.Stream:
+    """The stream object for a stream or a raw handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream
+
+
+def _record(stream, tensors) -> None:
+    """Tells the allocator that `stream` uses these tensors.  Nothing is known about how long the
+    stream behind a raw handle lives, and the allocator would ask it when a tensor is freed."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+
+
+def _takes_stream(call):
+    """Runs `call` with its `stream` argument as the current stream, so that what it allocates and
+    copies belongs to that stream."""
+    place = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if len(args) > place:
+            args, stream = args[:place], args[place]
+        if stream is None:
+            return call(*args, **kw)
+        tensors = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)]
+        dev = tensors[0].device if tensors and tensors[0].is_cuda else torch.device("cuda", torch.cuda.current_device())
+        caller = torch.cuda.current_stream(dev)
+        with torch.cuda.stream(_stream_on(stream, dev)):
+            out = call(*args, **kw)
+        _record(stream, tensors)
+        _record(caller, out if isinstance(out, tuple) else (out,))
+        return out
+    return run
+
+
 def _need(t: torch.Tensor, name: str, dtype=None, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
@@ -161,6 +210,7 @@ def _to_host(x):
     return h
 
 
+@_takes_stream
 def chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
               S0: Optional[torch.Tensor] = None, C: int = 64, gate: Optional[str] = None,
               O: Optional[torch.Tensor] = None, S_T: Optional[torch.Tensor] = None,
@@ -221,6 +271,7 @@ def chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     return O, S_T
 
 
+@_takes_stream
 def chunk_fwd_prologue(q_raw: torch.Tensor, k_raw: torch.Tensor, v: torch.Tensor, a: torch.Tensor,
                        A_log: torch.Tensor, dt_bias: torch.Tensor, b_logit: torch.Tensor,
                        S0: Optional[torch.Tensor] = None, C: int = 64, gate: Optional[str] = None,
@@ -285,6 +336,7 @@ def chunk_fwd_prologue(q_raw: torch.Tensor, k_raw: torch.Tensor, v: torch.Tensor
     return O, S_T
 
 
+@_takes_stream
 def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
                    S: torch.Tensor, o: Optional[torch.Tensor] = None, gate: Optional[str] = None,
                    stream=None) -> torch.Tensor:
@@ -318,6 +370,7 @@ def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     return o
 
 
+@_takes_stream
 def chunk_fwd_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,
                    w: torch.Tensor, S0: Optional[torch.Tensor] = None, C: int = 64, gate: Optional[str] = None,
                    O: Optional[torch.Tensor] = None, S_T: Optional[torch.Tensor] = None,
@@ -377,6 +430,7 @@ def chunk_fwd_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     return O, S_T
 
 
+@_takes_stream
 def recurrent_step_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,
                         w: torch.Tensor, S: torch.Tensor, o: Optional[torch.Tensor] = None,
                         gate: Optional[str] = None, stream=None) -> torch.Tensor:
@@ -409,6 +463,7 @@ def recurrent_step_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     return o
 
 
+@_takes_stream
 def chunk_fwd_gated(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
                     gate: torch.Tensor, norm_w: torch.Tensor, eps: float = 1e-6,
                     S0: Optional[torch.Tensor] = None, C: int = 64, gate_mode: Optional[str] = None,
@@ -470,6 +525,7 @@ def chunk_fwd_gated(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     return Y, S_T
 
 
+@_takes_stream
 def chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
               dO: torch.Tensor, S0: Optional[torch.Tensor] = None, dS_T: Optional[torch.Tensor] = None,
               C: int = 64, gate: Optional[str] = None, want_dS0: bool = True,

@@ -10,7 +10,7 @@ the formulas).  Differences in manner:
 * ``lengths`` (int32 ``[B]``) ends rows before T.  Behind a row's end inputs
   are not read and ``y`` is left as it is; a ``y`` made by the call is zero
   there.
-* Outputs and workspaces are made on the stream that the call runs on.
+* Outputs and workspaces are made on the stream that the call runs on (see the package about `stream`).
 * With a host ``x`` the inputs are copied to the current device and the results
   come back as new host tensors; an output that the caller gives has to lie on
   the device (a host one is refused), and the step calls, which update a state
@@ -23,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _DTYPES, _check, _to_device, _to_host, lib
+from . import _DTYPES, _check, _record, _stream_on, _to_device, _to_host, lib
 
 _ACTIVATIONS = {None: 0, "silu": 1}
 _F32, _I32 = torch.float32, torch.int32
@@ -73,19 +73,20 @@ def _elsewhere(call, x, stream, *args, outputs=()):
                 raise ValueError(f"{name} is a host tensor: a call with host inputs returns its results in new ones")
         index = torch.cuda.current_device()
     dev = torch.device("cuda", index)
-    if stream is None:
-        with torch.cuda.device(dev):
-            stream = torch.cuda.current_stream()
-    elif not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    caller = torch.cuda.current_stream(dev)
+    given = stream
+    stream = caller if stream is None else _stream_on(stream, dev)
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         if host:
             x = _to_device(x, dev)
             args = [_to_device(t, dev) if isinstance(t, torch.Tensor) else t for t in args]
         out = call(stream.cuda_stream, index, x, *args, **dict(outputs))
-        return tuple(_to_host(t) for t in out) if host else out
+        if host:
+            return tuple(_to_host(t) for t in out)
+    if given is not None:
+        _record(given, (x, *args, *(t for _, t in outputs)))
+        _record(caller, out if isinstance(out, tuple) else (out,))
+    return out
 
 
 def _ptr(t: Optional[torch.Tensor]):
