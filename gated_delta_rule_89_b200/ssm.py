@@ -491,6 +491,9 @@ def _scan_bwd(handle, index, x, dt, A, Bm, Cm, dy, D_skip, z, dt_bias, dt_softpl
         _dense(lengths, "lengths", (B,), index, _I32)
     dx, ddt, dz = _new(shape, ty, index), _new(shape, ty, index), None if z is None else _new(shape, ty, index)
     dB, dC, dA = _new(Bm.shape, ty, index), _new(Bm.shape, ty, index), _new((D, N), _F32, index)
+    if D == 0:      # the library has nothing to do: sums over no channels
+        dB.zero_()
+        dC.zero_()
     dD = None if D_skip is None else _new((D,), _F32, index)
     db = None if dt_bias is None else _new((D,), _F32, index)
     dh0 = None if h0 is None else _new((B, D, N), _F32, index)

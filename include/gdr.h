@@ -406,7 +406,8 @@ int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *
  *   dx, ddt, dz   [B,T,D]     dtype     (written, dense; zero behind a row's
  *                                       end); dz unused without z
  *   dB, dC        [B,T,G,N]   dtype     (written, dense), summed over the
- *                                       group's channels in fp32
+ *                                       group's channels in fp32; not
+ *                                       written when D is 0
  *   dA            [D,N]       float     (written)
  *   dD, ddt_bias  [D]         float     (written); NULL = not wanted
  *   dh0           [B,D,N]     float     (written); NULL = not wanted

@@ -179,3 +179,15 @@ def test_a_training_step_through_both():
     for got, want in ((dx, leaf[0].grad), (dw, leaf[1].grad), (db, leaf[2].grad)):
         # fp32 along chains of about 50 roundings each, whose terms partly cancel
         assert (got.double().cpu() - want).abs().max() <= 2e-5 * want.abs().max()
+
+
+def test_no_channels():
+    """Sums over no channels: dB and dC are zero, whatever their memory held."""
+    for dt in (BF, FP):
+        c = make(2, 5, 0, 16, dt=dt)
+        junk = [torch.full((2, 5, 1, 16), 7.0, dtype=dt, device="cuda") for _ in range(4)]
+        del junk
+        got = gradients(c, rnd(2, 5, 0, dtype=dt), rnd(2, 0, 16))
+        assert got["dB"].shape == got["dC"].shape == (2, 5, 1, 16)
+        assert not got["dB"].any() and not got["dC"].any()
+        assert got["dx"].shape == (2, 5, 0) and got["dA"].shape == (0, 16)
