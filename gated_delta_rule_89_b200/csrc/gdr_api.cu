@@ -486,6 +486,46 @@ int scan_sizes(int B, int T, int D, int G, int N, int dtype)
     return GDR_OK;
 }
 
+// Whether the dense block of `count` elements at `out` shares memory with one
+// of the B x H x T rows of `row` elements at `in` (elements of `bytes`).
+bool overlap(const void *out, long long count, const void *in, const gdr::RowStrides &s, int B, int H, int T,
+             long long row, size_t bytes)
+{
+    if (!out || !in || count <= 0 || row <= 0 || B <= 0 || H <= 0 || T <= 0) return false;
+    const long long e = (long long)bytes, first = (long long)(reinterpret_cast<uintptr_t>(in));
+    const long long lo = (long long)(reinterpret_cast<uintptr_t>(out)), hi = lo + count * e;
+    if (hi <= first || first + ((B - 1) * s.b + (H - 1) * s.h + (T - 1) * s.t + row) * e <= lo) return false;
+    for (int b = 0; b < B; ++b)
+        for (int h = 0; h < H; ++h) {
+            const long long base = first + (b * s.b + h * s.h) * e, step = s.t * e, before = lo - base - row * e;
+            // the first row that ends behind lo
+            const long long t = before < 0 || step == 0 ? 0 : before / step + 1, at = base + t * step;
+            if (t < T && at < hi && at + row * e > lo) return true;
+        }
+    return false;
+}
+
+// As overlap(), for outputs whose kernel reads every element of `in` in the
+// thread that later writes its place: those may be the same dense tensor.
+bool overlap_elsewhere(const void *out, long long count, const void *in, const gdr::BatchToken &s, int B, int T,
+                       long long row, size_t bytes)
+{
+    if (out == in && (T == 1 || s.t == row) && (B == 1 || s.b == T * row)) return false;
+    return overlap(out, count, in, {s.b, 0, s.t}, B, 1, T, row, bytes);
+}
+
+// Whether y lies in an input that the kernels may still read.
+bool scan_overlap(const gdr::ScanArgs &a)
+{
+    const size_t e = a.bf16 ? 2 : 4;
+    const long long outs = (long long)a.B * a.T * a.D, GN = (long long)a.G * a.N;
+    return overlap_elsewhere(a.y, outs, a.x, a.xs, a.B, a.T, a.D, e) ||
+           overlap_elsewhere(a.y, outs, a.dt, a.dts, a.B, a.T, a.D, e) ||
+           overlap_elsewhere(a.y, outs, a.z, a.zs, a.B, a.T, a.D, e) ||
+           overlap(a.y, outs, a.Bm, {a.bs.b, 0, a.bs.t}, a.B, 1, a.T, GN, e) ||
+           overlap(a.y, outs, a.Cm, {a.cs.b, 0, a.cs.t}, a.B, 1, a.T, GN, e);
+}
+
 gdr::BatchToken tokens_or_dense(const long long *s, int T, long long row)
 {
     if (s) return {s[0], s[1]};
@@ -512,6 +552,11 @@ GDR_API int gdr_short_conv_fwd(const void *x, const float *weight, const float *
     if (any_misaligned(rows, 4, elem_bytes(dtype)) || any_misaligned(words, 3, 4)) return GDR_ERR_ALIGNMENT;
     gdr::ConvArgs a = {x, rows_or_dense(x_strides, H, T, d), weight, bias, state, lengths, y, state_out,
                        B, H, T, d, W, act == GDR_ACT_SILU, dtype == GDR_BF16, lengths && zero_tail};
+    // y's rows are written while other threads still read x's rows around them
+    const long long outs = (long long)B * H * T * d, D = (long long)H * d;
+    if (overlap(y, outs, x, a.xs, B, H, T, d, elem_bytes(dtype)) ||
+        overlap(y, outs, state, {(W - 1) * D, 0, D}, B, 1, W - 1, D, elem_bytes(dtype)))
+        return GDR_ERR_INVALID_ARG;
     int launches = 0;
     const cudaError_t e = gdr::launch_short_conv_fwd(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -528,6 +573,10 @@ GDR_API int gdr_short_conv_step(const void *x, const float *weight, const float 
     if (any_misaligned(rows, 3, elem_bytes(dtype)) || any_misaligned(words, 2, 4)) return GDR_ERR_ALIGNMENT;
     gdr::ConvArgs a = {x, {x_stride, 0, 0}, weight, bias, state, nullptr, y, state,
                        B, 1, 1, D, W, act == GDR_ACT_SILU, dtype == GDR_BF16, false};
+    const size_t bytes = elem_bytes(dtype);
+    if (overlap_elsewhere(y, (long long)B * D, x, {x_stride, 0}, B, 1, D, bytes) ||
+        overlap(y, (long long)B * D, state, {(W - 1LL) * D, 0, D}, B, 1, W - 1, D, bytes))
+        return GDR_ERR_INVALID_ARG;
     int launches = 0;
     const cudaError_t e = gdr::launch_short_conv_step(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -557,6 +606,7 @@ GDR_API int gdr_short_conv_bwd(const void *x, const float *weight, const float *
         return GDR_ERR_ALIGNMENT;
     const size_t need = gdr_short_conv_bwd_workspace_size(B, H, T, d, W, dtype);
     if (ws_bytes < need || (need && !workspace)) return GDR_ERR_INVALID_ARG;
+    if (B > 0 && T > 0 && (dx == x || dx == dy)) return GDR_ERR_INVALID_ARG;   // read around the rows that are written
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (B == 0) {   // the sums over no rows
         cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)H * d * W, st);
@@ -600,6 +650,7 @@ GDR_API int gdr_ssm_scan_fwd(const void *x, const void *dt, const float *A, cons
                        tokens_or_dense(s ? s + 6 : s, T, (long long)G * N), tokens_or_dense(s ? s + 8 : s, T, D),
                        A, D_skip, dt_bias, h0, lengths, y, h_T, B, T, D, G, N, dt_softplus != 0, dtype == GDR_BF16,
                        workspace, lengths && zero_tail};
+    if (scan_overlap(a)) return GDR_ERR_INVALID_ARG;
     int launches = 0;
     const cudaError_t e = gdr::launch_ssm_scan_fwd(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);
@@ -623,6 +674,7 @@ GDR_API int gdr_ssm_scan_step(const void *x, const void *dt, const float *A, con
     gdr::ScanArgs a = {x, dt, Bm, Cm, z, {s[0], 0}, {s[1], 0}, {s[2], 0}, {s[3], 0}, {s[4], 0},
                        A, D_skip, dt_bias, nullptr, nullptr, y, h, B, 1, D, G, N, dt_softplus != 0,
                        dtype == GDR_BF16, nullptr, false};
+    if (scan_overlap(a)) return GDR_ERR_INVALID_ARG;
     int launches = 0;
     const cudaError_t e = gdr::launch_ssm_scan_step(a, static_cast<cudaStream_t>(stream), &launches);
     return finish(e, launches);

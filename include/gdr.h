@@ -325,6 +325,10 @@ int gdr_chunk_fwd_noalloc(const void *q, const void *k, const void *v, const flo
  * element only, float and int vectors to 4 bytes; they take 16-byte (8-byte)
  * accesses where pointers and strides allow it, one element at a time
  * otherwise.  B and D <= 2^20, T < 2^30, B T D < 2^40.
+ * Outputs share no memory with inputs, nor with one another, except where it
+ * says that they may: y (fwd and step) and, as far as it is the same pointer,
+ * the convolution's dx are checked (GDR_ERR_INVALID_ARG).  The scan's y and a
+ * step's y may be x, dt or z themselves if those are dense.
  */
 typedef enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
 

@@ -254,3 +254,25 @@ def test_feeds_the_gated_delta_rule():
     # the carried state is fp32 and chunks start at the same tokens: the same arithmetic
     err = (O[:, :, 128:].float() - O2.float()).abs().max() / O.float().abs().max()
     assert err <= 2e-2 and (S - S2).abs().max() <= 2e-2 * S.abs().max()
+
+
+def test_outputs_beside_and_in_the_inputs():
+    """y right behind x, or between far apart rows of x, is taken; y in x is not, but a step's may be x."""
+    D, T = 24, 40
+    buf = rnd(4, T, D, dtype=BF).cuda()
+    w = rnd(D, 4, seed=2).cuda()
+    ref, _ = gdr.short_conv_fwd(buf[:1].clone(), w)
+    y, _ = gdr.short_conv_fwd(buf[:1], w, y=buf[1:2])
+    assert torch.equal(y, ref) and torch.equal(buf[1:2], ref)
+    buf = rnd(4, T, D, dtype=BF).cuda()
+    far = buf[::3]                                 # rows 0 and 3; y is rows 1 and 2
+    ref, _ = gdr.short_conv_fwd(far.contiguous(), w)
+    gdr.short_conv_fwd(far, w, y=buf[1:3])
+    assert torch.equal(buf[1:3], ref)
+    for y in (buf[:2], buf[1:3]):
+        with pytest.raises(gdr.GDRError):
+            gdr.short_conv_fwd(buf[:2], w, y=y)
+    x, st = rnd(5, D, dtype=BF).cuda(), rnd(5, 3, D, dtype=BF, seed=3).cuda()
+    st2 = st.clone()
+    ref = gdr.short_conv_step(x, st, w)
+    assert torch.equal(gdr.short_conv_step(x, st2, w, y=x), ref) and torch.equal(x, ref) and torch.equal(st, st2)

@@ -158,3 +158,41 @@ def test_import_without_cuda_in_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(gdr.__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def at(n):
+    return P(0x100000 + n)
+
+
+def test_outputs_in_the_inputs_memory(L):
+    """An output that lies in rows which other threads still read is refused.  (Nothing here is launched: what
+    is allowed is tried on real memory in the GPU tests.)"""
+    def conv(x=GOOD, y=at(1 << 20), state=None, strides=None, B=2, H=2, T=10, d=8, dtype=0):
+        return L.gdr_short_conv_fwd(x, at(1 << 24), None, state, None, y, None, strides, 0, B, H, T, d, 4, 1, dtype, None)
+    size = 2 * 2 * 10 * 8 * 4
+    assert conv(y=GOOD) == INVALID
+    assert conv(y=at(size - 4)) == INVALID and conv(x=at(size - 4), y=GOOD) == INVALID
+    assert conv(state=at((1 << 20) + size - 16)) == INVALID and conv(state=at((1 << 20) - 16)) == INVALID
+    rows = longs(10 * 48, 8, 48)       # a third of a projection's rows; y in its last row
+    assert conv(strides=rows, y=at((19 * 48 + 8 + 7) * 4)) == INVALID
+
+    def bwd(dx, dy=at(1 << 20)):
+        return L.gdr_short_conv_bwd(GOOD, at(1 << 24), None, None, None, dy, None, dx, at(1 << 25), None, None, None,
+                                    None, None, 1, 1, 4, 8, 4, 1, 1, at(1 << 26), 1 << 40, None)
+    assert bwd(GOOD) == INVALID and bwd(at(1 << 20)) == INVALID
+
+    def conv_step(y, x=GOOD, xs=8):
+        return L.gdr_short_conv_step(x, at(1 << 24), None, at(1 << 22), y, xs, 3, 8, 4, 1, 0, None)
+    assert conv_step(at(4)) == INVALID and conv_step(GOOD, xs=16) == INVALID and conv_step(at(1 << 22)) == INVALID
+
+    def scan(y, z=None, strides=None):
+        return L.gdr_ssm_scan_fwd(GOOD, at(1 << 16), at(1 << 24), at(1 << 17), at(1 << 18), None, z, None, None, None, y,
+                                  None, strides, 0, 2, 10, 8, 1, 16, 1, 0, None, 0, None)
+    assert scan(at(4)) == INVALID and scan(at((1 << 16) - 4)) == INVALID and scan(at(1 << 17)) == INVALID
+    assert scan(at((1 << 18) + 2 * 10 * 16 * 4 - 4)) == INVALID and scan(at(1 << 19), z=at((1 << 19) + 8)) == INVALID
+    assert scan(GOOD, strides=longs(160, 16, 80, 8, 160, 16, 160, 16, 80, 8)) == INVALID     # x strided
+
+    def scan_step(y):
+        return L.gdr_ssm_scan_step(GOOD, at(1 << 16), at(1 << 24), at(1 << 17), at(1 << 18), None, None, None, at(1 << 20),
+                                   y, None, 2, 8, 1, 16, 1, 0, None)
+    assert scan_step(at(8)) == INVALID and scan_step(at(1 << 17)) == INVALID

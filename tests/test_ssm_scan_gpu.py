@@ -288,3 +288,26 @@ def test_a_whole_mixer():
     # the projections are library products whose order of sums may differ between the two runs
     y = torch.cat(outs, 1)
     assert (y - whole).abs().max() <= 1e-4 * whole.abs().max() and (h - h1).abs().max() <= 1e-4 * h.abs().max()
+
+
+@pytest.mark.parametrize("case", [dict(B=2, T=75, D=40), dict(B=1, T=700, D=40, dt=FP), dict(B=3, T=50, D=66, G=2),
+                                  dict(B=230, T=37, D=36)], ids=str)
+def test_y_in_place(case):
+    """y may be x, dt or z itself; one that meets them otherwise is refused."""
+    c = make(**case)
+    d = {k: cuda(v) for k, v in c.items()}
+    ref, h = gdr.ssm_scan_fwd(**d)
+    for k in ("x", "dt", "z"):
+        e = {**d, k: d[k].clone()}
+        y, h2 = gdr.ssm_scan_fwd(**e, y=e[k])
+        assert torch.equal(y, ref) and torch.equal(e[k], ref) and torch.equal(h, h2), k
+    wide = torch.zeros(2, *d["x"].shape, dtype=d["x"].dtype, device="cuda")
+    wide[0] = d["x"]
+    with pytest.raises(gdr.GDRError):
+        gdr.ssm_scan_fwd(**{**d, "x": wide[0]}, y=wide.view(-1)[8:8 + d["x"].numel()].view_as(d["x"]))
+    if case["B"] < 100:
+        one = {k: (v[:, 0].contiguous() if k in ("x", "dt", "z", "Bm", "Cm") else v) for k, v in d.items()
+               if k not in ("h0", "lengths")}
+        a, b = d["h0"].clone(), d["h0"].clone()
+        ref = gdr.ssm_scan_step(**one, h=a)
+        assert torch.equal(gdr.ssm_scan_step(**one, h=b, y=one["x"]), ref) and torch.equal(a, b)
