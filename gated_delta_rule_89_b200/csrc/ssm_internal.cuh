@@ -192,6 +192,18 @@ __device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
     return exp2_approx2(fma2(delta, A2, both(2e-8f)));
 }
 
+// decay2(delta, A2) h + v for the decay over a whole piece of a row.  Where a
+// state grows, that decay can pass fp32's range while the state is 0 or tiny
+// (0 has to stay 0), so what is above 2^126 goes to h first; elsewhere h is
+// multiplied by exactly 1.
+__device__ __forceinline__ f32x2 fold2(f32x2 delta, f32x2 A2, f32x2 h, f32x2 v)
+{
+    const f32x2 e = fma2(delta, A2, both(2e-8f));
+    const float lo = lo_f32(e), hi = hi_f32(e);
+    const f32x2 above = make_f32x2(fminf(fmaxf(lo - 126.f, 0.f), 127.f), fminf(fmaxf(hi - 126.f, 0.f), 127.f));
+    return fma2(exp2_approx2(make_f32x2(fminf(lo, 126.f), fminf(hi, 126.f))), mul2(exp2_approx2(above), h), v);
+}
+
 // log(1 + e) for e in [0, 1], as e times a polynomial of degree 9 in e (a
 // weighted least-squares fit to log(1 + e) / e, relative error 5e-9, so the
 // fp32 rounding of its evaluation, 1.6e-7, is what is left).  A logarithm of

@@ -150,8 +150,8 @@ ssm_scan_kernel(const ScanArgs a, const Pieces pc, int blocks_per_group)
                 for (int s = 1; s <= piece; ++s) {   // fold in the pieces ahead
                     const f32x2 sum = both(pc.sums[((size_t)s * a.B + b) * a.D + cfirst + ch + k]);
                     const ulonglong2 v = *(const ulonglong2 *)(pc.slots + s * slot + ak);
-                    h[k][0] = fma2(decay2(sum, A[k][0]), h[k][0], v.x);
-                    h[k][1] = fma2(decay2(sum, A[k][1]), h[k][1], v.y);
+                    h[k][0] = fold2(sum, A[k][0], h[k][0], v.x);
+                    h[k][1] = fold2(sum, A[k][1], h[k][1], v.y);
                 }
         }
         float sum[CPT] = {};

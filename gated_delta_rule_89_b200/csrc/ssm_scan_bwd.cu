@@ -191,8 +191,8 @@ ssm_bwd_kernel(const ScanBwdArgs a, const BwdParts parts, int blocks_per_group)
                 const f32x2 sum = both(pc.sums[((size_t)s * f.B + b) * f.D + c]);
                 f32x2 v0, v1;
                 order.load(pc.slots + (size_t)s * f.B * f.D * N + at, v0, v1);
-                carry0 = fma2(decay2(sum, A0), carry0, v0);
-                carry1 = fma2(decay2(sum, A1), carry1, v1);
+                carry0 = fold2(sum, A0, carry0, v0);
+                carry1 = fold2(sum, A1, carry1, v1);
             }
         // the stored state ahead of the sub-tile that comes next
         const size_t pstride = (size_t)f.D * N;

@@ -191,3 +191,22 @@ def test_no_channels():
         assert got["dB"].shape == got["dC"].shape == (2, 5, 1, 16)
         assert not got["dB"].any() and not got["dC"].any()
         assert got["dx"].shape == (2, 5, 0) and got["dA"].shape == (0, 16)
+
+
+@pytest.mark.parametrize("T,D,N", [(700, 40, 16), (400, 24, 8), (270, 12, 64)])
+def test_growing_states_across_pieces(T, D, N):
+    """States that grow (A > 0) by more than fp32 holds over a piece, where nothing has come in:
+    0 stays 0.  x is there for the last 8 tokens only and dy for the first 8, so the states and
+    their gradients are 0 or small wherever they are used."""
+    c = make(1, T, D, N, dt=FP, bias=False, state=False)
+    c["A"] = 4 + rnd(D, N, seed=50) * 0.1
+    c["dt"] = torch.ones(1, T, D)
+    c["x"][:, :-8] = 0
+    dy = rnd(1, T, D, seed=30)
+    y_ref, h_ref, by, bh = ssm.scan_fwd(**c, softplus=False)
+    y, h = gdr.ssm_scan_fwd(**{k: cuda(v) for k, v in c.items()}, dt_softplus=False)
+    near(y, y_ref, by, FP, "y")
+    near(h, h_ref, bh, FP, "h")
+    dy[:, 8:] = 0
+    got = check(c, dy, None, softplus=False)
+    assert got["dx"][:, :8].any() and not got["dx"][:, 8:].any()
