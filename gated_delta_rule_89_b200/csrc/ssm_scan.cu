@@ -492,20 +492,34 @@ int blocks_per_group(int D, int G, int N, int cpt)
     return (D / G + cb - 1) / cb;
 }
 
-// One or two channels a thread, by how the blocks fill the SMs (two on each
-// either way).  Measured at N = 16, bf16, in us per 4096 tokens: one channel
-// 260 for a full set of 296 blocks and 154 for half of one, two channels 467
-// and 287; so two are 10% faster where they fill the machine, and slower where
-// half of them would find no work (2 x 4096 channels: 260 and 287 us, 4 x 4096
-// channels: 527 and 467).
-int channels_per_thread(int B, int D, int G, int N)
+// Where two channels a thread can pay (with outputs; the passes without them
+// are 0% to 40% slower with two).  At N = 8 their shared memory leaves an SM
+// one block, and in fp32 at N = 16 they spill 536 bytes a thread: 2048 tokens
+// of 37888 channels, one and two channels a thread, N = 8: bf16 372 and 448 us,
+// fp32 388 and 847; 18944 channels, N = 16, fp32: 294 and 325.
+template <typename T, int N> constexpr bool kTwoChannels = sizeof(T) == 2 ? N >= 16 : N >= 32;
+
+// And whether they do, by how the blocks fill the SMs (two on each either way).
+// In us per 4096 tokens (N = 16, bf16): one channel 260 for a full set of 296
+// blocks and 154 for half of one, two channels 467 and 287; in fp32 at N = 64
+// half a set takes as long as a full one (but not one element at a time, where
+// the helpers bound it).  2048 tokens, with as many blocks of one channel a
+// thread as named, one and two channels a thread in us:
+//                     296          444          592          888
+//   N = 16, bf16   157  167     230  259     284  259     406  377
+//   N = 32, bf16   148  150     218  237     263  236     378  346
+//   N = 64, bf16   160  169     237  261     297  261     428  407
+//   N = 32, fp32   158  182     255  276     289  273     422  410
+//   N = 64, fp32   195  245     301  339     360  341     530  647
+// and one element at a time at 592: 364 302, 334 261, 391 267, 384 305, 457 341.
+template <typename T, int N, bool VECTOR> bool two_channels(int B, int D, int G)
 {
     const long long set = 2 * kSms, groups = (long long)B * G;
     auto cost = [&](int cpt, int full, int half) {
         const long long blocks = groups * blocks_per_group(D, G, N, cpt), rest = blocks % set;
         return blocks / set * full + (rest == 0 ? 0 : rest <= kSms ? half : full);
     };
-    return cost(2, 467, 287) < cost(1, 260, 154) ? 2 : 1;
+    return cost(2, 467, sizeof(T) == 4 && N == 64 && VECTOR ? 467 : 287) < cost(1, 260, 154);
 }
 
 // Few channels leave most of the machine idle; then a row is cut into pieces
@@ -520,7 +534,7 @@ int channels_per_thread(int B, int D, int G, int N)
 Pieces plan(int B, int T, int D, int G, int N, void *workspace)
 {
     Pieces p = {1, T, nullptr, nullptr, nullptr};
-    const long long blocks = (long long)B * G * blocks_per_group(D, G, N, channels_per_thread(B, D, G, N));
+    const long long blocks = (long long)B * G * blocks_per_group(D, G, N, 1);   // two channels a thread need more
     if (blocks > 0 && blocks * 2 <= kSms && T >= 8 * kUnit) {
         long long count = 4 * kSms / blocks;
         if (count > 64) count = 2 * kSms / blocks > 64 ? 2 * kSms / blocks : 64;
@@ -570,35 +584,33 @@ struct Extra {
     Pieces back = {};
 };
 
-template <typename T, int N, int CPT, bool VECTOR>
+template <typename T, int N, bool VECTOR>
 cudaError_t scan_typed(const ScanArgs &a, const Extra &x, cudaStream_t st, int *launches)
 {
     cudaError_t e = cudaSuccess;
     if (x.adjoint) {
-        e = run_scan<T, N, CPT, VECTOR, ADJOINT>(a, x.back, x.back.count - 1, st);
+        e = run_scan<T, N, 1, VECTOR, ADJOINT>(a, x.back, x.back.count - 1, st);
         if (e == cudaSuccess) *launches += 1;
         return e;
     }
     Pieces p = plan(a.B, a.T, a.D, a.G, N, a.workspace);
     if (p.count > 1) {
-        e = run_scan<T, N, CPT, VECTOR, LOCAL>(a, p, p.count - 1, st);
+        e = run_scan<T, N, 1, VECTOR, LOCAL>(a, p, p.count - 1, st);
         if (e != cudaSuccess) return e;
         *launches += 1;
     }
     p.points = x.points;
-    e = x.points ? run_scan<T, N, CPT, VECTOR, POINTS>(a, p, p.count, st)
-               : run_scan<T, N, CPT, VECTOR, FULL>(a, p, p.count, st);
-    if (e == cudaSuccess) *launches += 1;
-    return e;
+    *launches += 1;
+    if (x.points) return run_scan<T, N, 1, VECTOR, POINTS>(a, p, p.count, st);
+    if constexpr (kTwoChannels<T, N>)
+        if (two_channels<T, N, VECTOR>(a.B, a.D, a.G)) return run_scan<T, N, 2, VECTOR, FULL>(a, p, p.count, st);
+    return run_scan<T, N, 1, VECTOR, FULL>(a, p, p.count, st);
 }
 
 template <typename T, int N>
 cudaError_t scan_by_layout(const ScanArgs &a, const Extra &x, cudaStream_t st, int *launches)
 {
-    const bool v = scan_vectors<T>(a);
-    if (channels_per_thread(a.B, a.D, a.G, N) == 2)
-        return v ? scan_typed<T, N, 2, true>(a, x, st, launches) : scan_typed<T, N, 2, false>(a, x, st, launches);
-    return v ? scan_typed<T, N, 1, true>(a, x, st, launches) : scan_typed<T, N, 1, false>(a, x, st, launches);
+    return scan_vectors<T>(a) ? scan_typed<T, N, true>(a, x, st, launches) : scan_typed<T, N, false>(a, x, st, launches);
 }
 
 template <typename T, int N>

@@ -311,3 +311,25 @@ def test_y_in_place(case):
         a, b = d["h0"].clone(), d["h0"].clone()
         ref = gdr.ssm_scan_step(**one, h=a)
         assert torch.equal(gdr.ssm_scan_step(**one, h=b, y=one["x"]), ref) and torch.equal(a, b)
+
+
+# Two channels a thread are taken where twice the channels still fill two blocks on most SMs, in bf16 from
+# N = 16 and in fp32 from N = 32 on; a last block with one channel of a thread's two, and rows that end.
+@pytest.mark.parametrize("case", [
+    dict(B=230, T=35, D=36, N=16),
+    dict(B=230, T=35, D=41, N=16, lengths=[35, 3, 0, 32, 31] * 46),
+    dict(B=230, T=35, D=20, N=32),
+    dict(B=230, T=35, D=20, N=32, dt=FP, lengths=[35, 3, 0, 32, 31] * 46),
+    dict(B=230, T=35, D=17, N=32, dt=FP),
+    dict(B=230, T=35, D=12, N=64),
+    dict(B=230, T=35, D=12, N=64, dt=FP),
+    dict(B=230, T=35, D=9, N=64, dt=FP, lengths=[35, 3, 0, 32, 31] * 46),
+    dict(B=230, T=35, D=40, N=16, dt=FP),      # and sizes that would, of a type and N that do not
+    dict(B=230, T=35, D=72, N=8),
+], ids=str)
+def test_many_rows(case):
+    c = make(**case)
+    y_ref, h_ref, by, bh = ssm.scan_fwd(**c)
+    y, h = gdr.ssm_scan_fwd(**{k: cuda(v) for k, v in c.items()})
+    near(y, y_ref, by, c["x"].dtype, "y")
+    near(h, h_ref, bh, FP, "h")
