@@ -210,3 +210,37 @@ def test_growing_states_across_pieces(T, D, N):
     dy[:, 8:] = 0
     got = check(c, dy, None, softplus=False)
     assert got["dx"][:, :8].any() and not got["dx"][:, 8:].any()
+
+
+@pytest.mark.parametrize("case", [
+    dict(B=230, T=35, D=36, N=16, lengths=[35, 0, 1, 33, 32] * 46),
+    dict(B=230, T=33, D=69, N=8, dt=FP),
+    dict(B=115, T=40, D=36, N=32, G=2, z=False),
+    dict(B=230, T=20, D=10, N=64, skip=False),
+    dict(B=230, T=20, D=12, N=64, dt=FP),
+], ids=str)
+def test_many_rows(case):
+    """More blocks than the machine holds at a time, in the storing pass and in the walk."""
+    c = make(**case)
+    check(c, rnd(case["B"], case["T"], case["D"], dtype=c["x"].dtype, seed=30),
+          rnd(case["B"], case["D"], case["N"], seed=31))
+
+
+def test_pieces_are_taken():
+    """The cases above that are meant to be walked in pieces are: their workspace holds more than the
+    stored states, one block's share of dB and dC, and one part of dA, dD and ddt_bias a row."""
+    def pieces(B, T, D, N, G=1):
+        up = lambda n: (n + 255) // 256 * 256   # noqa: E731
+        groups = -(-(D // G) // (1024 // N))
+        rest = (gdr.ssm_scan_bwd_workspace_size(B, T, D, G, N) - gdr.ssm_scan_fwd_workspace_size(B, T, D, G, N) -
+                up(B * -(-T // 8) * D * N * 4) - up(groups * B * T * G * 2 * N * 4))
+        one = up(B * D * N * 4) + up(B * D * 8)
+        if rest == one:
+            return 1
+        for n in range(2, 200):      # as many parts, the gradients between the pieces, and their sums of delta
+            if rest == up(n * B * D * N * 4) * 2 + up(n * B * D * 8) + up(n * B * D * 4):
+                return n
+        raise AssertionError("the workspace is laid out otherwise")
+    assert pieces(2, 50, 68, 32) == 1 and pieces(230, 35, 36, 16) == 1
+    for size in ((1, 400, 40, 16), (3, 520, 20, 8, 2), (2, 300, 18, 32), (1, 270, 12, 64), (1, 700, 40, 16)):
+        assert pieces(*size) > 2, size
