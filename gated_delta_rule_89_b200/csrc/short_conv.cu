@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a, int
 // in registers, a block over its runs in shared memory, and the blocks'
 // partial sums are added by a second kernel in a fixed order, so the result
 // does not depend on scheduling.  4 x 4096 x 2048 bf16: 58 us, 201 MB at 3.5
-// TB/s; 128 registers a thread leave 16 warps on an SM, and half of the issue
-// slots are used (two channels a thread and more warps: 110 us and more).
+// TB/s (51 and, for the second kernel, 7); 128 registers a thread (and 28 bytes
+// spilled at W = 4) leave 16 warps on an SM, and half of the issue slots are used (two channels a thread and more warps: 110 us and more).
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int run, int runs, int across, float *part)
 {

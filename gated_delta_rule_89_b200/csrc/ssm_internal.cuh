@@ -205,8 +205,8 @@ __device__ __forceinline__ f32x2 fold2(f32x2 delta, f32x2 A2, f32x2 h, f32x2 v)
 }
 
 // log(1 + e) for e in [0, 1], as e times a polynomial of degree 9 in e (a
-// weighted least-squares fit to log(1 + e) / e, relative error 5e-9, so the
-// fp32 rounding of its evaluation, 1.6e-7, is what is left).  A logarithm of
+// weighted least-squares fit to log(1 + e) / e; with the coefficients rounded
+// to fp32 its relative error is 4e-8, and evaluated in fp32 1.6e-7).  A logarithm of
 // 1 + e would lose the digits of a small e in the sum; and time steps of 1e-3
 // have an e of 1e-3.  It also spares the special-function pipe one operation.
 // (One value at a time: the coefficients are then immediate operands, while

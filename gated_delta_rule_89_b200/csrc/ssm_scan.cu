@@ -492,11 +492,15 @@ int blocks_per_group(int D, int G, int N, int cpt)
     return (D / G + cb - 1) / cb;
 }
 
-// Where two channels a thread can pay (with outputs; the passes without them
-// are 0% to 40% slower with two).  At N = 8 their shared memory leaves an SM
-// one block, and in fp32 at N = 16 they spill 536 bytes a thread: 2048 tokens
-// of 37888 channels, one and two channels a thread, N = 8: bf16 372 and 448 us,
-// fp32 388 and 847; 18944 channels, N = 16, fp32: 294 and 325.
+// Where two channels a thread can pay: with outputs only (the pass that stores
+// states for the backward is never faster with two: a whole backward of 2048 x
+// 9472, bf16, N = 16, 544 and 606 us; N = 32, 1024 and 1022).  At N = 8 their
+// shared memory leaves an SM one block, and in fp32 at N = 16 they spill 536
+// bytes a thread: 2048 tokens of 37888 channels, one and two channels a thread,
+// N = 8: bf16 349 and 419 us, fp32 362 and 807; 18944 channels, N = 16, fp32:
+// 276 and 300.  (Kernels that are chosen spill too: in fp32 one channel a thread
+// 192 bytes at N = 8 and 16, two 532 at N = 32 and 876 at N = 64; in bf16 two
+// channels 140 bytes at N = 16 and 32, 420 at N = 64.)
 template <typename T, int N> constexpr bool kTwoChannels = sizeof(T) == 2 ? N >= 16 : N >= 32;
 
 // And whether they do, by how the blocks fill the SMs (two on each either way).
@@ -506,12 +510,12 @@ template <typename T, int N> constexpr bool kTwoChannels = sizeof(T) == 2 ? N >=
 // the helpers bound it).  2048 tokens, with as many blocks of one channel a
 // thread as named, one and two channels a thread in us:
 //                     296          444          592          888
-//   N = 16, bf16   157  167     230  259     284  259     406  377
-//   N = 32, bf16   148  150     218  237     263  236     378  346
-//   N = 64, bf16   160  169     237  261     297  261     428  407
-//   N = 32, fp32   158  182     255  276     289  273     422  410
-//   N = 64, fp32   195  245     301  339     360  341     530  647
-// and one element at a time at 592: 364 302, 334 261, 391 267, 384 305, 457 341.
+//   N = 16, bf16   140  146     211  239     265  241     388  359
+//   N = 32, bf16   127  129     198  215     244  217     360  327
+//   N = 64, bf16   142  149     216  242     276  244     411  386
+//   N = 32, fp32   140  164     236  254     272  254     403  392
+//   N = 64, fp32   173  217     278  319     341  321     508  624
+// and one element at a time at 592: 341 279, 312 239, 369 242, 366 285, 438 320.
 template <typename T, int N, bool VECTOR> bool two_channels(int B, int D, int G)
 {
     const long long set = 2 * kSms, groups = (long long)B * G;
@@ -527,10 +531,11 @@ template <typename T, int N, bool VECTOR> bool two_channels(int B, int D, int G)
 // with from a zero start, and the second starts every piece from the states
 // ahead of it.  That doubles the exponentials, so it pays from half the
 // machine down.  Two sets of blocks rather than one let the short rows of a
-// ragged batch make room for the long ones (2 x 20011 x 520 ragged 199 us with
-// one set, 175 with two; whole rows 198 and 198), up to 64 pieces: every piece
-// folds in all those ahead (128 channels x 65536 tokens: 113 us with 74 pieces,
-// 125 with 148).
+// ragged batch make room for the long ones (2 x 20011 x 520, N = 8, fp32, eight
+// draws of the short row's length: 201 us with one set at the mean, 184 with
+// two, 168 to 202; whole rows 201 and 201), up to 64 pieces: every piece folds
+// in all those ahead (128 channels x 65536 tokens, N = 16, bf16: 116 us with 74
+// pieces, 134 with 148).
 Pieces plan(int B, int T, int D, int G, int N, void *workspace)
 {
     Pieces p = {1, T, nullptr, nullptr, nullptr};

@@ -22,9 +22,10 @@
 // warp by an exchange that halves the number of values at each step and end
 // with the helpers too.  Blocks' parts of dB and dC, and batch rows' parts of
 // dA, dD and ddt_bias, are added by a last kernel in a fixed order: no atomics,
-// equal calls give equal bits.  4 x 4096 x 2048, N = 16, bf16: 920 us, of which
-// the storing pass takes about 190, the walk 720 (69% of the issue slots, 250
-// instructions per 16 channels and token) and the last kernel 14.
+// equal calls give equal bits.  4 x 4096 x 2048, N = 16, bf16: 911 us, of which
+// the storing pass takes about 180, the walk 720 (72% of the issue slots of the
+// SMs that have a block: 128 of 148; 250 instructions per 16 channels and token)
+// and the last kernel 14.
 #include <type_traits>
 
 #include "ssm_internal.cuh"
