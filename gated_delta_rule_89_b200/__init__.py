@@ -159,7 +159,8 @@ def _record(stream, tensors) -> None:
 def _takes_stream(call):
     """Runs `call` with its `stream` argument as the current stream, so that what it allocates and
     copies belongs to that stream."""
-    place = list(inspect.signature(call).parameters).index("stream")
+    names = list(inspect.signature(call).parameters)
+    place = names.index("stream")
 
     @functools.wraps(call)
     def run(*args, stream=None, **kw):
@@ -167,12 +168,13 @@ def _takes_stream(call):
             args, stream = args[:place], args[place]
         if stream is None:
             return call(*args, **kw)
-        tensors = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)]
-        dev = tensors[0].device if tensors and tensors[0].is_cuda else torch.device("cuda", torch.cuda.current_device())
+        first = args[0] if args else kw.get(names[0])      # says where the call runs: a host one, on the current device
+        dev = first.device if isinstance(first, torch.Tensor) and first.is_cuda else \
+            torch.device("cuda", torch.cuda.current_device())
         caller = torch.cuda.current_stream(dev)
         with torch.cuda.stream(_stream_on(stream, dev)):
             out = call(*args, **kw)
-        _record(stream, tensors)
+        _record(stream, (*args, *kw.values()))
         _record(caller, out if isinstance(out, tuple) else (out,))
         return out
     return run

@@ -6,16 +6,11 @@ import pytest
 import torch
 
 import gated_delta_rule_89_b200 as gdr
+from test_ssm_scan_gpu import BF, rnd
 
 pytestmark = pytest.mark.gpu
 
-BF, FP = torch.bfloat16, torch.float32
 B, H, T, D, N = 2, 2, 192, 128, 16
-
-
-def rnd(*shape, dtype=FP, seed=0, scale=1.0):
-    g = torch.Generator().manual_seed(seed)
-    return (torch.randn(*shape, generator=g) * scale).to(dtype)
 
 
 def rule(**kw):
@@ -142,3 +137,25 @@ def test_stream_by_position_and_by_handle():
         o = gdr.recurrent_step(*a, None, None, s)
         torch.cuda.synchronize()
         assert torch.equal(o, ref)
+
+
+@pytest.mark.parametrize("name", ["chunk_fwd", "chunk_bwd", "short_conv_bwd", "ssm_scan_fwd", "ssm_scan_bwd"])
+def test_captured_on_a_forked_stream(name):
+    """A call on a stream that a capture has forked to, replayed on new inputs, beside an eager call."""
+    call, make, drop = CALLS[name]
+    d = {k: v.cuda() for k, v in make().items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call(**d, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        out = as_tuple(call(**d, stream=side))
+        torch.cuda.current_stream().wait_stream(side)
+    for scale in (1.0, 0.5):
+        d[drop].mul_(scale)
+        g.replay()
+        eager = as_tuple(call(**d))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))
