@@ -156,9 +156,21 @@ def _record(stream, tensors) -> None:
                 t.record_stream(stream)
 
 
+def _on_stream(stream, call, first, *args, **kw):
+    """call(*args, **kw) with `stream` current, so that what it allocates and copies belongs to that
+    stream.  `first` says where the call runs: a host tensor, on the current device."""
+    dev = first.device if isinstance(first, torch.Tensor) and first.is_cuda else \
+        torch.device("cuda", torch.cuda.current_device())
+    caller = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(_stream_on(stream, dev)):
+        out = call(*args, **kw)
+    _record(stream, (*args, *kw.values()))
+    _record(caller, out if isinstance(out, tuple) else (out,))
+    return out
+
+
 def _takes_stream(call):
-    """Runs `call` with its `stream` argument as the current stream, so that what it allocates and
-    copies belongs to that stream."""
+    """Runs `call` on the stream of its `stream` argument, if there is one."""
     names = list(inspect.signature(call).parameters)
     place = names.index("stream")
 
@@ -168,15 +180,7 @@ def _takes_stream(call):
             args, stream = args[:place], args[place]
         if stream is None:
             return call(*args, **kw)
-        first = args[0] if args else kw.get(names[0])      # says where the call runs: a host one, on the current device
-        dev = first.device if isinstance(first, torch.Tensor) and first.is_cuda else \
-            torch.device("cuda", torch.cuda.current_device())
-        caller = torch.cuda.current_stream(dev)
-        with torch.cuda.stream(_stream_on(stream, dev)):
-            out = call(*args, **kw)
-        _record(stream, (*args, *kw.values()))
-        _record(caller, out if isinstance(out, tuple) else (out,))
-        return out
+        return _on_stream(stream, call, args[0] if args else kw.get(names[0]), *args, **kw)
     return run
 
 
@@ -338,7 +342,6 @@ def chunk_fwd_prologue(q_raw: torch.Tensor, k_raw: torch.Tensor, v: torch.Tensor
     return O, S_T
 
 
-@_takes_stream
 def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
                    S: torch.Tensor, o: Optional[torch.Tensor] = None, gate: Optional[str] = None,
                    stream=None) -> torch.Tensor:
@@ -347,6 +350,8 @@ def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     q, k [B,H,dk], v [B,H,dv] (fp32 or bf16); g fp32 [B,H,dk] (per-channel)
     or [B,H] (scalar); beta fp32 [B,H].  Returns o [B,H,dv] in v's dtype.
     """
+    if stream is not None:
+        return _on_stream(stream, recurrent_step, S, q, k, v, g, beta, S, o, gate)
     dev = S.device
     if gate is None:
         gate = "per_channel" if g.dim() == 3 else "scalar"
@@ -432,7 +437,6 @@ def chunk_fwd_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     return O, S_T
 
 
-@_takes_stream
 def recurrent_step_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, b: torch.Tensor,
                         w: torch.Tensor, S: torch.Tensor, o: Optional[torch.Tensor] = None,
                         gate: Optional[str] = None, stream=None) -> torch.Tensor:
@@ -441,6 +445,8 @@ def recurrent_step_gdr2(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     q, k, b [B,H,dk], v, w [B,H,dv] (fp32 or bf16, one dtype); g fp32
     [B,H,dk] or [B,H].  Returns o [B,H,dv] in v's dtype.
     """
+    if stream is not None:
+        return _on_stream(stream, recurrent_step_gdr2, S, q, k, v, g, b, w, S, o, gate)
     dev = S.device
     if gate is None:
         gate = "per_channel" if g.dim() == 3 else "scalar"
